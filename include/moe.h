@@ -14,6 +14,11 @@
  *   moe_grouped_ffn  every expert's FFN over its rows as one grouped GEMM
  *   moe_combine      gate-weighted sum back into token order
  *
+ * moe_layer_decode runs all of it for a few tokens (up to
+ * MOE_DECODE_MAX_TOKENS) in one kernel.  moe_layer_forward_lora,
+ * moe_grouped_ffn_lora and moe_layer_decode take low-rank adapters of many
+ * requests beside the shared expert projections (moe_lora).
+ *
  * Around them: moe_reroute (over-capacity re-routing between two
  * permutations), moe_update_sel_bias (sliding-window selection-bias update),
  * moe_quantize_rows_e4m3 (the W8A8 activation quantiser on its own),
@@ -66,6 +71,7 @@ typedef enum { MOE_ACT_GELU = 0, MOE_ACT_SWIGLU = 1 } moe_act;
 #define MOE_STATUS_BAD_EXPERT_ID 0x2u   /* moe_permute saw an id outside [0,E) */
 #define MOE_STATUS_TIMEOUT 0x4u         /* a bounded device wait gave up */
 #define MOE_STATUS_BAD_GROUP 0x8u       /* a group table entry out of range */
+#define MOE_STATUS_BAD_ADAPTER 0x20u    /* an adapter id outside [-1, num_adapters): treated as -1 */
 #define MOE_STATUS_DEBUG_CHECK 0x10u    /* an internal invariant check failed (the MOE_DEBUG
                                            build's checks; the re-route assignment's epoch bound) */
 
@@ -176,6 +182,42 @@ typedef struct {
   const float *s_up;
   const float *s_down;
 } moe_weights;
+
+/*
+ * Low-rank adapters of many requests beside the expert projections, which all
+ * requests share.  A projection W[e] (out x in) of a token with adapter a
+ * becomes
+ *     W[e] + scale[a] * B[a][e] A[a][e],
+ * A[a][e] rank x in, B[a][e] out x rank, for each projection whose pair is
+ * given (a NULL pair: that projection has no adapters; at least one pair must
+ * be given).  The product is taken as scale * B (A x): the projection's own
+ * product stays that of the shared weights, and the adapter's share is added
+ * to its fp32 sum before the channel bias, the activation or the combine.
+ *   num_adapters N >= 1; rank r: a multiple of 8, at most MOE_LORA_MAX_RANK
+ *     (adapters of smaller ranks are padded with zeros).
+ *   All pointers DEVICE, 16-byte aligned (scale 4-byte), row-major bf16:
+ *     a_gate, a_up [N][E+ns][r][d], b_gate, b_up [N][E+ns][h][r],
+ *     a_down [N][E+ns][r][h], b_down [N][E+ns][d][r]; scale fp32 [N]
+ *     (alpha / rank).  GeLU layers (w1, w2) use a_up, b_up for w1 and a_down,
+ *     b_down for w2; their a_gate, b_gate must be NULL.
+ * The calls that take it also take adapter_of_token int32 [S] (DEVICE): the
+ * adapter of each token, -1 for none.  An id outside [-1, N) counts as -1 and
+ * sets MOE_STATUS_BAD_ADAPTER.  Adapters need bf16 activations (bf16 or E4M3
+ * expert weights, W8A8 included; the adapters themselves are bf16 and are
+ * multiplied with the bf16 tokens and hidden rows).
+ */
+#define MOE_LORA_MAX_RANK 128
+typedef struct {
+  int32_t num_adapters;
+  int32_t rank;
+  const void *a_gate;
+  const void *b_gate;
+  const void *a_up;
+  const void *b_up;
+  const void *a_down;
+  const void *b_down;
+  const float *scale;
+} moe_lora;
 
 /* Number of rows of the routed row space: S*K, or E*C + S*K with capacity
  * (primary block of E*C rows, then the overflow region).  The shared expert,
@@ -360,6 +402,51 @@ moe_status moe_layer_forward(const moe_desc *desc, const moe_weights *w, const v
 moe_status moe_layer_forward_timed(const moe_desc *desc, const moe_weights *w, const void *x, void *y,
                                    int32_t *topk_idx, float *topk_w, int32_t *counts, void *ws, size_t ws_bytes,
                                    void *stream, void *const *events);
+
+/*
+ * The whole layer for a few tokens in ONE kernel: S <= MOE_DECODE_MAX_TOKENS.
+ * Same arguments, weights and results (up to fp32 summation order) as
+ * moe_layer_forward, plus optional adapters (lora and adapter_of_token, both
+ * NULL or both given).  The expert outputs are summed in fp32 (no bf16
+ * rounding per expert); the hidden rows are bf16 (two-term or W8A8 codes with
+ * E4M3 weights), as in moe_grouped_ffn.  A capacity changes nothing (no row
+ * is dropped).
+ *   Supported: bf16 activations with bf16 weights (SwiGLU, GeLU) or E4M3
+ *   weights (SwiGLU, act_quant 0 or 1, d and h multiples of 16), reroute = 0;
+ *   MOE_ERR_UNSUPPORTED otherwise, MOE_ERR_INVALID_ARG for a larger S.
+ *   ws: at least moe_decode_workspace_size bytes (lora may be NULL there),
+ *   256-byte aligned, zeroed once by moe_workspace_init; its first 256 bytes
+ *   hold the status block and the kernel's grid barrier, which every call
+ *   leaves as it found it.  Calls that share a workspace must be ordered on
+ *   one stream.  The kernel is a cooperative launch with one CTA per SM (it
+ *   starts once every CTA fits); it may be captured into a graph.  After
+ *   MOE_STATUS_TIMEOUT call moe_workspace_init before using the workspace
+ *   again.
+ */
+#define MOE_DECODE_MAX_TOKENS 64
+moe_status moe_decode_workspace_size(const moe_desc *desc, const moe_lora *lora, size_t *bytes);
+moe_status moe_layer_decode(const moe_desc *desc, const moe_weights *w, const moe_lora *lora,
+                            const int32_t *adapter_of_token, const void *x, void *y, int32_t *topk_idx,
+                            float *topk_w, int32_t *counts, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The grouped expert FFN and the whole layer with adapters, for any number of
+ * tokens.  moe_grouped_ffn_lora: moe_grouped_ffn's arguments plus lora,
+ * adapter_of_token [S] and token_of_row [R] (moe_permute's output; rows with
+ * -1 are not computed).  moe_layer_forward_lora: moe_layer_forward's arguments
+ * plus lora and adapter_of_token.  The adapters' inner products A x are summed
+ * in fp32 and kept as bf16 between the two products.  ws: at least
+ * moe_lora_workspace_size bytes, otherwise as moe_layer_forward.  reroute = 1
+ * is supported by both as by the calls without adapters.
+ */
+moe_status moe_lora_workspace_size(const moe_desc *desc, const moe_lora *lora, size_t *bytes);
+moe_status moe_grouped_ffn_lora(const moe_desc *desc, const moe_weights *w, const moe_lora *lora,
+                                const int32_t *adapter_of_token, const void *x_perm, const int32_t *offsets,
+                                const int32_t *token_of_row, const void *x, void *y_perm, void *ws, size_t ws_bytes,
+                                void *stream);
+moe_status moe_layer_forward_lora(const moe_desc *desc, const moe_weights *w, const moe_lora *lora,
+                                  const int32_t *adapter_of_token, const void *x, void *y, int32_t *topk_idx,
+                                  float *topk_w, int32_t *counts, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * Sliding-window expert load and the aux-loss-free selection-bias update

@@ -275,6 +275,68 @@ moe_status permute_impl(const moe_desc& d, const void* x, const int32_t* topk_id
   return s != MOE_OK ? s : debug_check(a, st);
 }
 
+// Adapters of one call: the kernels' view, and the regions behind the layer's
+// own workspace that hold the inner products and the deltas.
+struct LoraCall {
+  LoraParams p{};
+  const int32_t* token_of_row = nullptr;
+  void* u = nullptr;
+  void* delta = nullptr;
+};
+
+struct LoraLayout {
+  size_t u, delta, total;
+};
+
+LoraLayout lora_layout(const moe_desc& d, const moe_lora& l) {
+  const int64_t rows = routed_rows(d) + static_cast<int64_t>(d.num_shared) * d.num_tokens;
+  const int64_t pairs = d.activation == MOE_ACT_SWIGLU ? 2 : 1;
+  const int64_t cols = pairs * d.d_ff > d.d_model ? pairs * d.d_ff : d.d_model;
+  LoraLayout L;
+  L.u = make_layout(d).total;
+  L.delta = L.u + align_up(static_cast<size_t>(rows * pairs * l.rank) * 2);
+  L.total = L.delta + align_up(static_cast<size_t>(rows * cols) * 2);
+  return L;
+}
+
+// Checks of a moe_lora against the layer (not of device data).
+moe_status lora_status(const moe_desc& d, const moe_lora* l) {
+  if (l == nullptr || l->num_adapters < 1) return MOE_ERR_INVALID_ARG;
+  if (l->rank < 8 || l->rank % 8 != 0 || l->rank > MOE_LORA_MAX_RANK) return MOE_ERR_INVALID_ARG;
+  if (d.act_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status lora_pointers(const moe_desc& d, const moe_lora& l, const int32_t* ids) {
+  const void* pair[3][2] = {{l.a_gate, l.b_gate}, {l.a_up, l.b_up}, {l.a_down, l.b_down}};
+  bool any = false;
+  for (int m = 0; m < 3; ++m) {
+    if ((pair[m][0] == nullptr) != (pair[m][1] == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (pair[m][0] == nullptr) continue;
+    if (m == 0 && d.activation == MOE_ACT_GELU) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(pair[m][0]) || !aligned16(pair[m][1])) return MOE_ERR_INVALID_ARG;
+    any = true;
+  }
+  if (!any || l.scale == nullptr || (reinterpret_cast<uintptr_t>(l.scale) & 3) != 0) return MOE_ERR_INVALID_ARG;
+  if (ids == nullptr || (reinterpret_cast<uintptr_t>(ids) & 3) != 0) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+LoraParams lora_params(const moe_lora& l, const int32_t* ids) {
+  LoraParams p{};
+  p.n = l.num_adapters;
+  p.r = l.rank;
+  const void* a[3] = {l.a_gate, l.a_up, l.a_down};
+  const void* b[3] = {l.b_gate, l.b_up, l.b_down};
+  for (int m = 0; m < 3; ++m) {
+    p.a[m] = a[m];
+    p.b[m] = b[m];
+  }
+  p.scale = l.scale;
+  p.ids = ids;
+  return p;
+}
+
 // Record stage event `i` of `events` (moe_layer_forward_timed), if given.
 bool record(void* const* events, int i, cudaStream_t st) {
   if (events == nullptr || events[i] == nullptr) return true;
@@ -283,7 +345,7 @@ bool record(void* const* events, int i, cudaStream_t st) {
 
 moe_status ffn_impl(const moe_desc& d, const moe_weights& w, const void* x_perm, const int32_t* offsets, const void* x,
                     void* y_perm, void* ws, cudaStream_t st, bool groups_ready = false, bool a_quantized = false,
-                    void* const* events = nullptr) {
+                    void* const* events = nullptr, const LoraCall* lora = nullptr) {
   const Layout L = make_layout(d);
   const int S = d.num_tokens, E = d.num_experts, h = d.d_ff, dm = d.d_model;
   if (S == 0) return MOE_OK;
@@ -415,11 +477,45 @@ moe_status ffn_impl(const moe_desc& d, const moe_weights& w, const void* x_perm,
                                       at<float>(ws, L.sh), Rt, nullptr, nullptr, nullptr, 0, h, g.max_total_rows,
                                       terms, status, st);
   };
+  // adapters: their share of a GEMM's sums, from its bf16 input rows (the
+  // tokens themselves where the row gather wrote codes)
+  auto adapt = [&](GemmArgs& g, int m0, int pairs, const void* src, bool by_token, const void* src_shared) {
+    if (lora == nullptr || (lora->p.a[m0] == nullptr && (pairs == 1 || lora->p.a[m0 + 1] == nullptr)))
+      return cudaSuccess;
+    LoraRowsArgs a{};
+    a.lora = lora->p;
+    a.m0 = m0;
+    a.pairs = pairs;
+    a.groups = g.groups;
+    a.num_groups = g.num_groups;
+    a.shared_slab = d.num_shared ? E : -1;
+    a.slabs = slabs;
+    a.token_of_row = lora->token_of_row;
+    a.S = S;
+    a.src = src;
+    a.src_by_token = by_token;
+    a.src_shared = src_shared;
+    a.rows = Rt;
+    a.max_total_rows = g.max_total_rows;
+    a.K = g.K;
+    a.N = g.N;
+    a.u = lora->u;
+    a.delta = lora->delta;
+    a.status = status;
+    a.num_sms = sms;
+    g.delta = lora->delta;
+    return launch_lora_rows(a, st);
+  };
   if (terms && !a_quantized && (err = quant_up(up)) != cudaSuccess) return MOE_ERR_CUDA;
+  const bool swiglu = d.activation == MOE_ACT_SWIGLU;
+  if ((err = adapt(up, swiglu ? 0 : 1, swiglu ? 2 : 1, a_quantized ? x : x_perm, a_quantized,
+                   d.num_shared ? x : nullptr)) != cudaSuccess)
+    return MOE_ERR_CUDA;
   if (!record(events, 3, st)) return MOE_ERR_CUDA;
   if ((err = run(up)) != cudaSuccess) return MOE_ERR_CUDA;
   if (!record(events, 4, st)) return MOE_ERR_CUDA;
   if (terms && (err = quant_down(down)) != cudaSuccess) return MOE_ERR_CUDA;
+  if ((err = adapt(down, 2, 1, hidden, false, nullptr)) != cudaSuccess) return MOE_ERR_CUDA;
   if (!record(events, 5, st)) return MOE_ERR_CUDA;
   if ((err = run(down)) != cudaSuccess) return MOE_ERR_CUDA;
   if (!record(events, 6, st)) return MOE_ERR_CUDA;
@@ -473,9 +569,11 @@ bool weights_ok(const moe_desc& d, const moe_weights* w) {
 }
 
 // The layer call (moe_layer_forward), recording the stage events of
-// moe_layer_forward_timed when `events` is given.
+// moe_layer_forward_timed when `events` is given, with the adapters of
+// moe_layer_forward_lora when `lora` is given (desc already checked).
 moe_status layer_impl(const moe_desc* desc, const moe_weights* w, const void* x, void* y, int32_t* topk_idx,
-                      float* topk_w, int32_t* counts, void* ws, size_t ws_bytes, void* stream, void* const* events) {
+                      float* topk_w, int32_t* counts, void* ws, size_t ws_bytes, void* stream, void* const* events,
+                      LoraCall* lora = nullptr) {
   moe_status s = validate(desc);
   if (s != MOE_OK) return s;
   if ((s = check_ws(*desc, ws, ws_bytes)) != MOE_OK) return s;
@@ -491,6 +589,7 @@ moe_status layer_impl(const moe_desc* desc, const moe_weights* w, const void* x,
   int32_t* offs = at<int32_t>(ws, L.offsets);
   int32_t* ros = at<int32_t>(ws, L.row_of_slot);
   int32_t* tor = at<int32_t>(ws, L.token_of_row);
+  if (lora != nullptr) lora->token_of_row = tor;
   void* x_perm = at<void>(ws, L.x_perm);
   void* y_perm = at<void>(ws, L.y_perm);
   if (!record(events, 0, st)) return MOE_ERR_CUDA;
@@ -514,14 +613,24 @@ moe_status layer_impl(const moe_desc* desc, const moe_weights* w, const void* x,
                                st) != cudaSuccess)
       return MOE_ERR_CUDA;
     if (!record(events, 2, st)) return MOE_ERR_CUDA;
-    if ((s = ffn_impl(d, *w, x_perm, offs, x, y_perm, ws, st, true, true, events)) != MOE_OK) return s;
+    if ((s = ffn_impl(d, *w, x_perm, offs, x, y_perm, ws, st, true, true, events, lora)) != MOE_OK) return s;
   } else {
     if ((s = permute_impl(d, x, idx, cnt, offs, ros, tor, x_perm, ws, st, true)) != MOE_OK) return s;
     if (!record(events, 2, st)) return MOE_ERR_CUDA;
-    if ((s = ffn_impl(d, *w, x_perm, offs, x, y_perm, ws, st, true, false, events)) != MOE_OK) return s;
+    if ((s = ffn_impl(d, *w, x_perm, offs, x, y_perm, ws, st, true, false, events, lora)) != MOE_OK) return s;
   }
   if ((s = combine_impl(d, y_perm, ros, gates, y, st, at<StatusBlock>(ws, L.status))) != MOE_OK) return s;
   return record(events, 7, st) ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// What moe_layer_decode takes.
+moe_status decode_status(const moe_desc* desc) {
+  const moe_status s = validate(desc);
+  if (s != MOE_OK) return s;
+  if (desc->num_tokens > MOE_DECODE_MAX_TOKENS) return MOE_ERR_INVALID_ARG;
+  if (desc->act_dtype != MOE_BF16 || desc->reroute != 0) return MOE_ERR_UNSUPPORTED;
+  if (desc->weight_dtype == MOE_E4M3 && a_terms(*desc) == 0) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
 }
 
 }  // namespace
@@ -649,6 +758,127 @@ moe_status moe_layer_forward_timed(const moe_desc* desc, const moe_weights* w, c
   return layer_impl(desc, w, x, y, topk_idx, topk_w, counts, ws, ws_bytes, stream, events);
 }
 
+moe_status moe_lora_workspace_size(const moe_desc* desc, const moe_lora* lora, size_t* bytes) {
+  moe_status s = validate(desc);
+  if (s != MOE_OK) return s;
+  if ((s = lora_status(*desc, lora)) != MOE_OK) return s;
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = lora_layout(*desc, *lora).total;
+  return MOE_OK;
+}
+
+moe_status moe_grouped_ffn_lora(const moe_desc* desc, const moe_weights* w, const moe_lora* lora,
+                                const int32_t* adapter_of_token, const void* x_perm, const int32_t* offsets,
+                                const int32_t* token_of_row, const void* x, void* y_perm, void* ws, size_t ws_bytes,
+                                void* stream) {
+  NvtxRange nvtx("moe_grouped_ffn_lora");
+  moe_status s = validate(desc);
+  if (s != MOE_OK) return s;
+  if ((s = lora_status(*desc, lora)) != MOE_OK) return s;
+  if ((s = check_ws(*desc, ws, ws_bytes)) != MOE_OK) return s;
+  const LoraLayout L = lora_layout(*desc, *lora);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (desc->num_tokens == 0) return MOE_OK;
+  if (!weights_ok(*desc, w) || x_perm == nullptr || offsets == nullptr || y_perm == nullptr || token_of_row == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (desc->num_shared && x == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x_perm) || !aligned16(y_perm) || (x && !aligned16(x))) return MOE_ERR_INVALID_ARG;
+  if ((s = lora_pointers(*desc, *lora, adapter_of_token)) != MOE_OK) return s;
+  LoraCall call;
+  call.p = lora_params(*lora, adapter_of_token);
+  call.token_of_row = token_of_row;
+  call.u = at<void>(ws, L.u);
+  call.delta = at<void>(ws, L.delta);
+  return ffn_impl(*desc, *w, x_perm, offsets, x, y_perm, ws, static_cast<cudaStream_t>(stream), false, false, nullptr,
+                  &call);
+}
+
+moe_status moe_layer_forward_lora(const moe_desc* desc, const moe_weights* w, const moe_lora* lora,
+                                  const int32_t* adapter_of_token, const void* x, void* y, int32_t* topk_idx,
+                                  float* topk_w, int32_t* counts, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("moe_layer_forward_lora");
+  moe_status s = validate(desc);
+  if (s != MOE_OK) return s;
+  if ((s = lora_status(*desc, lora)) != MOE_OK) return s;
+  if ((s = check_ws(*desc, ws, ws_bytes)) != MOE_OK) return s;
+  const LoraLayout L = lora_layout(*desc, *lora);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (desc->num_tokens == 0) return MOE_OK;
+  if ((s = lora_pointers(*desc, *lora, adapter_of_token)) != MOE_OK) return s;
+  LoraCall call;
+  call.p = lora_params(*lora, adapter_of_token);
+  call.u = at<void>(ws, L.u);
+  call.delta = at<void>(ws, L.delta);
+  return layer_impl(desc, w, x, y, topk_idx, topk_w, counts, ws, ws_bytes, stream, nullptr, &call);
+}
+
+moe_status moe_decode_workspace_size(const moe_desc* desc, const moe_lora* lora, size_t* bytes) {
+  moe_status s = decode_status(desc);
+  if (s != MOE_OK) return s;
+  if (lora != nullptr && (s = lora_status(*desc, lora)) != MOE_OK) return s;
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  const moe_desc& d = *desc;
+  *bytes = decode_workspace_bytes(d.num_tokens, d.d_model, d.num_experts, d.top_k, d.d_ff, d.num_shared, a_terms(d),
+                                  lora != nullptr ? lora->rank : 0);
+  return MOE_OK;
+}
+
+moe_status moe_layer_decode(const moe_desc* desc, const moe_weights* w, const moe_lora* lora,
+                            const int32_t* adapter_of_token, const void* x, void* y, int32_t* topk_idx,
+                            float* topk_w, int32_t* counts, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("moe_layer_decode");
+  size_t need = 0;
+  moe_status s = moe_decode_workspace_size(desc, lora, &need);
+  if (s != MOE_OK) return s;
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0 || ws_bytes < need)
+    return MOE_ERR_WORKSPACE;
+  const moe_desc& d = *desc;
+  if (d.num_tokens == 0) return MOE_OK;
+  if (x == nullptr || y == nullptr || !aligned16(x) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  if (!weights_ok(d, w) || w->w_router == nullptr || !aligned16(w->w_router)) return MOE_ERR_INVALID_ARG;
+  if ((lora == nullptr) != (adapter_of_token == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (lora != nullptr && (s = lora_pointers(d, *lora, adapter_of_token)) != MOE_OK) return s;
+  DecodeArgs a{};
+  a.S = d.num_tokens;
+  a.d = d.d_model;
+  a.E = d.num_experts;
+  a.K = d.top_k;
+  a.h = d.d_ff;
+  a.num_shared = d.num_shared;
+  a.score_fn = d.score_fn;
+  a.renormalize = d.renormalize;
+  a.num_groups = d.num_groups;
+  a.topk_groups = d.topk_groups;
+  a.tau = d.temperature == 0.0f ? 1.0f : d.temperature;
+  a.activation = d.activation;
+  a.terms = a_terms(d);
+  a.x = x;
+  a.w_router = w->w_router;
+  a.router_bias = w->router_bias;
+  a.sel_bias = w->sel_bias;
+  if (d.activation == MOE_ACT_SWIGLU) {
+    a.w_in[0] = w->w_gate;
+    a.w_in[1] = w->w_up;
+    a.w_out = w->w_down;
+    a.s_in[0] = w->s_gate;
+    a.s_in[1] = w->s_up;
+    a.s_out = w->s_down;
+  } else {
+    a.w_in[0] = w->w1;
+    a.w_out = w->w2;
+    a.b_in = w->b1;
+    a.b_out = w->b2;
+  }
+  if (lora != nullptr) a.lora = lora_params(*lora, adapter_of_token);
+  a.y = y;
+  a.topk_idx = topk_idx;
+  a.topk_w = topk_w;
+  a.counts = counts;
+  a.ws = ws;
+  a.num_sms = num_sms();
+  return cuda_status(launch_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
 moe_status moe_load_stats(const moe_desc* desc, const int32_t* counts, double* stats, void* stream) {
   NvtxRange nvtx("moe_load_stats");
   const moe_status s = validate(desc);
@@ -701,7 +931,7 @@ moe_status moe_get_status(const void* ws, void* stream, uint32_t* flags, int32_t
   if (flags) *flags = host.flags;
   if (counters) memcpy(counters, host.counters, sizeof(host.counters));
   const uint32_t errors = MOE_STATUS_NONFINITE_LOGIT | MOE_STATUS_BAD_EXPERT_ID | MOE_STATUS_TIMEOUT |
-                          MOE_STATUS_BAD_GROUP | MOE_STATUS_DEBUG_CHECK;
+                          MOE_STATUS_BAD_GROUP | MOE_STATUS_BAD_ADAPTER | MOE_STATUS_DEBUG_CHECK;
   return (host.flags & errors) ? MOE_ERR_DEVICE_STATUS : MOE_OK;
 }
 

@@ -41,6 +41,7 @@ struct TcParams {
   int tma_out;         // 1: the output tensor map is valid (full 32-row quarters use bulk tensor stores)
   const float* row_scale;         // E4M3 activations: per-row scale of the A operand rows (nullptr: none)
   const float* row_scale_shared;  // ... of the shared expert's A rows (indexed by row within the group)
+  const __nv_bfloat16* delta;     // adapters' share of the sums [out_rows][pcols] (LORA kernels)
   StatusBlock* status;
 };
 
@@ -92,14 +93,17 @@ __device__ __forceinline__ bool group_ok(const GroupEntry& g, const TcParams& p)
 
 // Epilogue of split-K sums: gate/up sums g, u (SwiGLU) or sums v, with the
 // row scale rs, channel scales and bias of column n + j.
-template <int EPI>
+// dg, du: the adapters' share of the two sums (LORA).
+template <int EPI, bool LORA>
 __device__ __forceinline__ float splitk_out(const TcParams& p, int64_t sbase, int n, int j, float g, float u,
-                                            float rs) {
+                                            float rs, float dg, float du) {
   float gv = g * rs;
   if (p.scale0 != nullptr) gv *= p.scale0[sbase + n + j];
+  if (LORA) gv += dg;
   if (EPI == EPI_SWIGLU) {
     float uv = u * rs;
     if (p.scale1 != nullptr) uv *= p.scale1[sbase + n + j];
+    if (LORA) uv += du;
     return gv / (1.0f + __expf(-gv)) * uv;
   }
   if (EPI == EPI_GELU_BIAS || EPI == EPI_BIAS) gv += p.bias[sbase + n + j];
@@ -137,11 +141,18 @@ __device__ __forceinline__ void splitk_sums4(const float* src, int64_t off, int6
   }
 }
 
+__device__ __forceinline__ void bf16x4_to_f32(const uint2& w, float* f) {
+  f[0] = __uint_as_float(w.x << 16);
+  f[1] = __uint_as_float(w.x & 0xFFFF0000u);
+  f[2] = __uint_as_float(w.y << 16);
+  f[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+
 // Split-K finalize: for every valid row of every group, sum the partial slices
 // in split order and apply the epilogue; one thread per four output columns.
 // Exits at once when the GEMM ran without a split.  Launched under
 // programmatic dependent launch: it waits for the GEMM before reading.
-template <int EPI>
+template <int EPI, bool LORA>
 __global__ void __launch_bounds__(256) splitk_finalize_kernel(TcParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -161,11 +172,17 @@ __global__ void __launch_bounds__(256) splitk_finalize_kernel(TcParams p) {
   const float* src = p.partial + orow * p.pcols + n;
   float4 g, u;
   splitk_sums4<EPI == EPI_SWIGLU>(src, N, slice, ks, g, u);
+  float dg[4] = {0.f, 0.f, 0.f, 0.f}, du[4] = {0.f, 0.f, 0.f, 0.f};
+  if (LORA) {
+    const __nv_bfloat16* dl = p.delta + orow * p.pcols + n;
+    bf16x4_to_f32(*reinterpret_cast<const uint2*>(dl), dg);
+    if (EPI == EPI_SWIGLU) bf16x4_to_f32(*reinterpret_cast<const uint2*>(dl + N), du);
+  }
   float o[4];
-  o[0] = splitk_out<EPI>(p, sbase, n, 0, g.x, u.x, rs);
-  o[1] = splitk_out<EPI>(p, sbase, n, 1, g.y, u.y, rs);
-  o[2] = splitk_out<EPI>(p, sbase, n, 2, g.z, u.z, rs);
-  o[3] = splitk_out<EPI>(p, sbase, n, 3, g.w, u.w, rs);
+  o[0] = splitk_out<EPI, LORA>(p, sbase, n, 0, g.x, u.x, rs, dg[0], du[0]);
+  o[1] = splitk_out<EPI, LORA>(p, sbase, n, 1, g.y, u.y, rs, dg[1], du[1]);
+  o[2] = splitk_out<EPI, LORA>(p, sbase, n, 2, g.z, u.z, rs, dg[2], du[2]);
+  o[3] = splitk_out<EPI, LORA>(p, sbase, n, 3, g.w, u.w, rs, dg[3], du[3]);
   if (p.out_f32) {
     *reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow * N + n) = make_float4(o[0], o[1], o[2], o[3]);
   } else {

@@ -144,6 +144,13 @@ __device__ __forceinline__ UnitInfo decode_unit(const SmemCtl& s, const TcParams
   return ui;
 }
 
+// Element j of 32 bf16 values held as four 16-byte pieces.
+__device__ __forceinline__ float delta_at(const uint4 (&d)[4], int j) {
+  const uint4& q = d[j >> 3];
+  const uint32_t w = (j & 4) ? ((j & 2) ? q.w : q.z) : ((j & 2) ? q.y : q.x);
+  return __uint_as_float((j & 1) ? (w & 0xFFFF0000u) : (w << 16));
+}
+
 // Epilogue of one 32-row quarter of a tile: thread `lane` owns accumulator
 // row `row` (and its activation row scale rs).  The per-column operands
 // (weight-channel scales, biases) are loaded once per 32-column chunk, lane j
@@ -154,7 +161,10 @@ __device__ __forceinline__ UnitInfo decode_unit(const SmemCtl& s, const TcParams
 // last) writes each 32-column chunk into its shared-memory box and stores it
 // with one bulk tensor store (full 128-byte lines instead of 32 scattered
 // 16-byte pieces per store instruction); a partial quarter stores row by row.
-template <int EPI>
+//
+// LORA: the adapters' share of the row's sums (bf16, 64 contiguous bytes per
+// chunk and lane) is added before the bias and the activation.
+template <int EPI, bool LORA>
 __device__ __forceinline__ void epilogue_store(const TcParams& p, const TileInfo& ti, uint32_t tbase, int row,
                                                bool valid, int lane, int half, const CUtensorMap* tm_out,
                                                uint8_t* ebuf) {
@@ -176,6 +186,16 @@ __device__ __forceinline__ void epilogue_store(const TcParams& p, const TileInfo
     }
     uint32_t r0[32];
     float v[32];
+    uint4 dl[4], dl1[4];  // delta of this lane's row, columns n .. n + 31 (and N + n ..); zero where there is none
+    if (LORA) {
+      const __nv_bfloat16* d0 = p.delta + orow * p.pcols + n;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = valid && n + 8 * j + 8 <= N;
+        dl[j] = in ? ldg16(d0 + 8 * j) : make_uint4(0, 0, 0, 0);
+        if (EPI == EPI_SWIGLU) dl1[j] = in ? ldg16(d0 + N + 8 * j) : make_uint4(0, 0, 0, 0);
+      }
+    }
     if (EPI == EPI_SWIGLU) {
       uint32_t r1[32];
       tmem_ld_32x32b_x32(tbase + c * 32, r0);
@@ -183,8 +203,12 @@ __device__ __forceinline__ void epilogue_store(const TcParams& p, const TileInfo
       tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        const float g = __uint_as_float(r0[j]) * rs * __shfl_sync(0xFFFFFFFFu, cs0, j);
-        const float u = __uint_as_float(r1[j]) * rs * __shfl_sync(0xFFFFFFFFu, cs1, j);
+        float g = __uint_as_float(r0[j]) * rs * __shfl_sync(0xFFFFFFFFu, cs0, j);
+        float u = __uint_as_float(r1[j]) * rs * __shfl_sync(0xFFFFFFFFu, cs1, j);
+        if (LORA) {
+          g += delta_at(dl, j);
+          u += delta_at(dl1, j);
+        }
         v[j] = __fdividef(g, 1.0f + __expf(-g)) * u;
       }
     } else {
@@ -193,6 +217,7 @@ __device__ __forceinline__ void epilogue_store(const TcParams& p, const TileInfo
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         float z = __uint_as_float(r0[j]) * rs * __shfl_sync(0xFFFFFFFFu, cs0, j);
+        if (LORA) z += delta_at(dl, j);
         if (kBias) z += __shfl_sync(0xFFFFFFFFu, cb, j);
         if (EPI == EPI_GELU_BIAS) z = 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
         v[j] = z;
@@ -260,7 +285,7 @@ __device__ __forceinline__ void epilogue_partial(const TcParams& p, const TileIn
   }
 }
 
-template <int EPI, bool F8>
+template <int EPI, bool F8, bool LORA>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
                            const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
@@ -490,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (ks > 1)
           epilogue_partial<EPI>(p, ti, tbase, row, valid, ui.split, half);
         else
-          epilogue_store<EPI>(p, ti, tbase, row, valid, lane, half, &tmOut, epi_smem + (warp - 2) * kEpiWarpBytes);
+          epilogue_store<EPI, LORA>(p, ti, tbase, row, valid, lane, half, &tmOut, epi_smem + (warp - 2) * kEpiWarpBytes);
       }
       tc_fence_before();
       mbar_arrive(&s.tempty[acc]);
@@ -506,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int EPI, bool F8>
-cudaError_t launch_epi(const CUtensorMap& mA, const CUtensorMap& mA2, const CUtensorMap& mB0, const CUtensorMap& mB1,
+template <int EPI, bool F8, bool LORA>
+cudaError_t launch_one(const CUtensorMap& mA, const CUtensorMap& mA2, const CUtensorMap& mB0, const CUtensorMap& mB1,
                        const CUtensorMap& mOut, const TcParams& p, int grid, int bma, int stages, size_t smem,
                        int64_t max_group_rows, cudaStream_t stream) {
   static std::atomic<uint64_t> attr_set{0};  // one bit per device ordinal (host threads may launch concurrently)
@@ -515,20 +540,29 @@ cudaError_t launch_epi(const CUtensorMap& mA, const CUtensorMap& mA2, const CUte
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(attr_set.load(std::memory_order_relaxed) & (1ull << dev))) {
-    e = cudaFuncSetAttribute(grouped_gemm_tc_kernel<EPI, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(grouped_gemm_tc_kernel<EPI, F8, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemLimitTc));
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   // programmatic dependent launch: the prologue may overlap the previous kernel
-  e = launch_pdl(grouped_gemm_tc_kernel<EPI, F8>, dim3(grid), dim3(kThreads), smem, stream, mA,
+  e = launch_pdl(grouped_gemm_tc_kernel<EPI, F8, LORA>, dim3(grid), dim3(kThreads), smem, stream, mA,
                  mA2, mB0, mB1, mOut, p, bma, stages);
   if (e != cudaSuccess) return e;
   if ((e = cudaGetLastError()) != cudaSuccess || p.max_ksplit <= 1) return e;
   dim3 fgrid((p.N + 1023) / 1024, static_cast<unsigned>(max_group_rows), p.num_groups);
-  e = launch_pdl(splitk_finalize_kernel<EPI>, fgrid, dim3(256), 0, stream, p);
+  e = launch_pdl(splitk_finalize_kernel<EPI, LORA>, fgrid, dim3(256), 0, stream, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+template <int EPI, bool F8>
+cudaError_t launch_epi(const CUtensorMap& mA, const CUtensorMap& mA2, const CUtensorMap& mB0, const CUtensorMap& mB1,
+                       const CUtensorMap& mOut, const TcParams& p, int grid, int bma, int stages, size_t smem,
+                       int64_t max_group_rows, cudaStream_t stream) {
+  if (p.delta != nullptr)
+    return launch_one<EPI, F8, true>(mA, mA2, mB0, mB1, mOut, p, grid, bma, stages, smem, max_group_rows, stream);
+  return launch_one<EPI, F8, false>(mA, mA2, mB0, mB1, mOut, p, grid, bma, stages, smem, max_group_rows, stream);
 }
 
 }  // namespace

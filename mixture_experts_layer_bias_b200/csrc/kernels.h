@@ -131,6 +131,7 @@ struct GemmArgs {
   int a_terms;              // fp8: 2 = A rows hold two-term codes [c1 | c2] (2K codes), summed in one accumulator
   const float* row_scale;        // [a rows] per-row scale of A (fp8 only)
   const float* row_scale_shared; // [S] per-row scale of the shared expert's A rows (fp8 only)
+  const void* delta;        // adapters' share, bf16 [out_rows][N] (SwiGLU: [out_rows][2N], gate then up), or nullptr
   StatusBlock* status;
 };
 cudaError_t launch_grouped_gemm_tc(const GemmArgs& a, int num_sms, cudaStream_t stream);
@@ -176,6 +177,74 @@ cudaError_t launch_bias_update(int S, int E, int K, int window, const int32_t* t
 // MOE_NUM_LOAD_STATS doubles from counts[E] (one CTA; see moe_load_stats).
 cudaError_t launch_load_stats(int E, int64_t slots, int capacity, const int32_t* counts, double* out,
                               cudaStream_t stream);
+
+// --- adapters ----------------------------------------------------------------
+// Low-rank adapters of the expert projections (moe_lora): pair m = 0 gate,
+// 1 up (w1 of GeLU layers), 2 down (w2); a[m] nullptr: no adapters there.
+struct LoraParams {
+  int n, r;                // adapters, rank (0 adapters: none)
+  const void* a[3];        // bf16 [n][slabs][r][in]
+  const void* b[3];        // bf16 [n][slabs][out][r]
+  const float* scale;      // [n]
+  const int32_t* ids;      // [S]: adapter of each token, -1 = none
+};
+
+// Inner products u = A row of every row of the groups, then the outer ones
+// delta = scale * B u, for `pairs` pairs from pair m0 (2: gate and up, N
+// columns each; 1: one).  Row i of a group is row r = out_row0 + i of the row
+// space; its token is token_of_row[r] (i for the shared expert's group) and
+// its input row: src row r, src row `token` (src_by_token), or, for the shared
+// expert's group, src_shared row i when given.  delta rows of tokens without
+// an adapter are zero.
+struct LoraRowsArgs {
+  LoraParams lora;
+  int m0, pairs;
+  const GroupEntry* groups;
+  int num_groups, shared_slab, slabs;
+  const int32_t* token_of_row;
+  int S;
+  const void* src;
+  int src_by_token;
+  const void* src_shared;
+  int64_t rows;            // rows of the row space
+  int64_t max_total_rows;  // bound of the rows of all groups together
+  int K, N;                // input and output width
+  void* u;                 // bf16 [rows][pairs][r]
+  void* delta;             // bf16 [rows][pairs * N]
+  StatusBlock* status;
+  int num_sms;
+};
+cudaError_t launch_lora_rows(const LoraRowsArgs& a, cudaStream_t stream);
+
+// --- the layer for a few tokens ------------------------------------------------
+constexpr int kDecodeMaxCtas = 160;  // CTAs of the cooperative kernel (one per SM; a B200 has 148)
+struct DecodeArgs {
+  int S, d, E, K, h, num_shared;
+  int score_fn, renormalize, num_groups, topk_groups;
+  float tau;
+  int activation;
+  int terms;  // 0: bf16 weights; 1 (W8A8), 2 (two-term codes): E4M3 weights
+  const void* x;
+  const void* w_router;
+  const float* router_bias;
+  const float* sel_bias;
+  const void* w_in[2];      // gate, up (SwiGLU) or w1, nullptr (GeLU)
+  const void* w_out;        // down or w2
+  const float* s_in[2];     // E4M3 channel scales of w_in
+  const float* s_out;
+  const float* b_in;        // GeLU: b1, b2
+  const float* b_out;
+  LoraParams lora;
+  void* y;
+  int32_t* topk_idx;        // optional outputs
+  float* topk_w;
+  int32_t* counts;
+  void* ws;
+  int num_sms;
+};
+// Workspace bytes of launch_decode for this shape (lora_rank 0: no adapters).
+size_t decode_workspace_bytes(int S, int d, int E, int K, int h, int num_shared, int terms, int lora_rank);
+cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 
 // --- combine -----------------------------------------------------------------
 struct CombineArgs {

@@ -1,8 +1,8 @@
-"""A buffer-owning wrapper around moe_layer_forward.
+"""A buffer-owning wrapper around moe_layer_forward and moe_layer_decode.
 
-``MoELayer`` keeps the descriptor, the weight pointers and a workspace sized
-by the library, so a forward pass is one C-ABI call on the current stream.
-Torch only provides the device memory and the stream.
+``MoELayer`` keeps the descriptor, the weight pointers, optional adapters and a
+workspace sized by the library, so a forward pass is one C-ABI call on the
+current stream.  Torch only provides the device memory and the stream.
 """
 from __future__ import annotations
 
@@ -13,14 +13,25 @@ from .synthetic import LayerConfig, desc_dict
 
 
 class MoELayer:
-    def __init__(self, cfg: LayerConfig, weights: dict, device="cuda", S=None, with_outputs=True):
+    def __init__(self, cfg: LayerConfig, weights: dict, device="cuda", S=None, with_outputs=True, adapters: dict = None):
+        """adapters: the tensors of ops.make_lora; forward and decode then take
+        adapter_ids, int32 [S], the adapter of each token (-1: none)."""
         self.cfg = cfg
         self.S = cfg.S if S is None else S
         self.device = torch.device(device)
         self.desc = ops.make_desc(**desc_dict(cfg, self.S))
         self.tensors = weights
         self.weights = ops.make_weights(weights)
-        nbytes = ops.moe_workspace_size(self.desc)
+        self.adapter_tensors = adapters
+        self.lora = None if adapters is None else ops.make_lora(adapters)
+        if self.lora is None:
+            nbytes = ops.moe_workspace_size(self.desc)
+        else:
+            nbytes = ops.moe_lora_workspace_size(self.desc, self.lora)
+        try:
+            nbytes = max(nbytes, ops.moe_decode_workspace_size(self.desc, self.lora))
+        except ops.MoeError:
+            pass  # not a layer that moe_layer_decode takes: decode() will say so
         self.ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         ops.moe_workspace_init(self.ws)
         adt = torch.float32 if cfg.act_dtype == 0 else torch.bfloat16
@@ -31,8 +42,27 @@ class MoELayer:
             self.topk_w = torch.empty((self.S, cfg.K), dtype=torch.float32, device=self.device)
             self.counts = torch.empty((cfg.E,), dtype=torch.int32, device=self.device)
 
-    def forward(self, x: torch.Tensor, y: torch.Tensor = None, stream=None) -> torch.Tensor:
+    def _ids(self, adapter_ids):
+        if (adapter_ids is None) != (self.lora is None):
+            raise ValueError("adapter_ids go with a layer made with adapters")
+        if adapter_ids is not None and (adapter_ids.dtype != torch.int32 or tuple(adapter_ids.shape) != (self.S,)
+                                        or not adapter_ids.is_contiguous()):
+            raise ValueError("adapter_ids must be a contiguous int32 tensor [S]")
+        return adapter_ids
+
+    def decode(self, x: torch.Tensor, y: torch.Tensor = None, stream=None, adapter_ids=None) -> torch.Tensor:
+        """The layer for a few tokens (S <= ops.MOE_DECODE_MAX_TOKENS) in one kernel."""
         out = self.y if y is None else y
+        ops.moe_layer_decode(self.desc, self.weights, self.lora, self._ids(adapter_ids), x, out, self.topk_idx,
+                             self.topk_w, self.counts, self.ws, stream)
+        return out
+
+    def forward(self, x: torch.Tensor, y: torch.Tensor = None, stream=None, adapter_ids=None) -> torch.Tensor:
+        out = self.y if y is None else y
+        if self._ids(adapter_ids) is not None:
+            ops.moe_layer_forward_lora(self.desc, self.weights, self.lora, adapter_ids, x, out, self.topk_idx,
+                                       self.topk_w, self.counts, self.ws, stream)
+            return out
         ops.moe_layer_forward(self.desc, self.weights, x, out, self.topk_idx, self.topk_w, self.counts, self.ws,
                               stream)
         return out

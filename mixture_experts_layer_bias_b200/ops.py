@@ -19,7 +19,8 @@ _lib = None
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE_STATUS = range(6)
 MOE_STATUS_NONFINITE_LOGIT, MOE_STATUS_BAD_EXPERT_ID, MOE_STATUS_TIMEOUT, MOE_STATUS_BAD_GROUP = 1, 2, 4, 8
-MOE_STATUS_DEBUG_CHECK = 0x10
+MOE_STATUS_DEBUG_CHECK, MOE_STATUS_BAD_ADAPTER = 0x10, 0x20
+MOE_DECODE_MAX_TOKENS, MOE_LORA_MAX_RANK = 64, 128
 MOE_NUM_COUNTERS = 8
 COUNTER_NAMES = ("nonfinite", "bad_id", "timeout", "overflow_rows", "rerouted")
 
@@ -33,7 +34,11 @@ WEIGHT_FIELDS = ("w_router", "router_bias", "sel_bias", "w1", "b1", "w2", "b2", 
 EXPORTED = ("moe_routed_rows", "moe_workspace_size", "moe_workspace_init", "moe_route", "moe_permute",
             "moe_permute_static", "moe_grouped_ffn", "moe_combine", "moe_layer_forward", "moe_layer_forward_timed",
             "moe_load_stats", "moe_bias_state_size", "moe_bias_state_init", "moe_update_sel_bias",
-            "moe_quantize_rows_e4m3", "moe_split_rows_e4m3", "moe_reroute", "moe_get_status", "moe_strerror")
+            "moe_quantize_rows_e4m3", "moe_split_rows_e4m3", "moe_reroute", "moe_get_status", "moe_strerror",
+            "moe_decode_workspace_size", "moe_layer_decode", "moe_lora_workspace_size", "moe_grouped_ffn_lora",
+            "moe_layer_forward_lora")
+
+LORA_FIELDS = ("a_gate", "b_gate", "a_up", "b_up", "a_down", "b_down", "scale")
 
 MOE_NUM_STAGE_EVENTS = 8
 MOE_NUM_LOAD_STATS = 6
@@ -46,6 +51,10 @@ class MoeDesc(ctypes.Structure):
 
 class MoeWeights(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in WEIGHT_FIELDS]
+
+
+class MoeLora(ctypes.Structure):
+    _fields_ = [("num_adapters", ctypes.c_int32), ("rank", ctypes.c_int32)] + [(f, ctypes.c_void_p) for f in LORA_FIELDS]
 
 
 class MoeError(RuntimeError):
@@ -63,7 +72,7 @@ def lib():
         raise RuntimeError(f"{_LIB_PATH} is missing: build it with `python -m mixture_experts_layer_bias_b200.build`")
     L = ctypes.CDLL(_LIB_PATH)
     P, I, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
-    pd, pw = ctypes.POINTER(MoeDesc), ctypes.POINTER(MoeWeights)
+    pd, pw, pl = ctypes.POINTER(MoeDesc), ctypes.POINTER(MoeWeights), ctypes.POINTER(MoeLora)
     sig = {
         "moe_routed_rows": (ctypes.c_int64, [pd]),
         "moe_workspace_size": (I, [pd, ctypes.POINTER(ctypes.c_size_t)]),
@@ -84,6 +93,11 @@ def lib():
         "moe_reroute": (I, [pd, P, P, P, P, P, SZ, P]),
         "moe_get_status": (I, [P, P, ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(ctypes.c_int32)]),
         "moe_strerror": (ctypes.c_char_p, [I]),
+        "moe_decode_workspace_size": (I, [pd, pl, ctypes.POINTER(ctypes.c_size_t)]),
+        "moe_layer_decode": (I, [pd, pw, pl, P, P, P, P, P, P, P, SZ, P]),
+        "moe_lora_workspace_size": (I, [pd, pl, ctypes.POINTER(ctypes.c_size_t)]),
+        "moe_grouped_ffn_lora": (I, [pd, pw, pl, P, P, P, P, P, P, P, SZ, P]),
+        "moe_layer_forward_lora": (I, [pd, pw, pl, P, P, P, P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -122,6 +136,35 @@ def make_weights(tensors: dict) -> MoeWeights:
     for f in WEIGHT_FIELDS:
         setattr(w, f, _ptr(tensors.get(f)))
     return w
+
+
+def make_lora(tensors: dict) -> MoeLora:
+    """Adapters struct from a dict of bf16 tensors a_gate [N][E+ns][r][d],
+    b_gate [N][E+ns][h][r], a_up, b_up, a_down, b_down (missing pairs -> NULL)
+    and scale fp32 [N]; the number of adapters and the rank come from their
+    shapes.  The caller keeps the tensors alive."""
+    first = next((tensors[f] for f in LORA_FIELDS if f.startswith("a_") and tensors.get(f) is not None), None)
+    if first is None:
+        raise ValueError("make_lora: no adapter pair given")
+    if first.dim() != 4:
+        raise ValueError("make_lora: adapter stacks have the shape [adapters][experts][rank][in]")
+    lora = MoeLora()
+    lora.num_adapters, lora.rank = int(first.shape[0]), int(first.shape[2])
+    slabs = int(first.shape[1])
+    for f in LORA_FIELDS:
+        t = tensors.get(f)
+        if t is not None:
+            want = torch.float32 if f == "scale" else torch.bfloat16
+            shape = (lora.num_adapters,) if f == "scale" else (lora.num_adapters, slabs, t.shape[2], t.shape[3])
+            rank = lora.rank if f == "scale" else t.shape[2 if f.startswith("a_") else 3]
+            if t.dtype != want or tuple(t.shape) != shape or rank != lora.rank or not t.is_contiguous():
+                raise ValueError(f"make_lora: {f} has the wrong type, shape or layout")
+        setattr(lora, f, _ptr(t))
+    return lora
+
+
+def _byref(struct):
+    return None if struct is None else ctypes.byref(struct)
 
 
 def _stream(stream) -> Optional[int]:
@@ -211,6 +254,44 @@ def moe_layer_forward_timed(desc, weights, x, y, topk_idx, topk_w, counts, ws, e
     _check(lib().moe_layer_forward_timed(ctypes.byref(desc), ctypes.byref(weights), _ptr(x), _ptr(y), _ptr(topk_idx),
                                          _ptr(topk_w), _ptr(counts), p, n, _stream(stream), handles),
            "moe_layer_forward_timed")
+
+
+def moe_decode_workspace_size(desc: MoeDesc, lora: Optional[MoeLora] = None) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_decode_workspace_size(ctypes.byref(desc), _byref(lora), ctypes.byref(n)),
+           "moe_decode_workspace_size")
+    return int(n.value)
+
+
+def moe_layer_decode(desc, weights, lora, adapter_of_token, x, y, topk_idx, topk_w, counts, ws, stream=None):
+    """The whole layer for up to MOE_DECODE_MAX_TOKENS tokens in one kernel
+    (lora and adapter_of_token may both be None)."""
+    p, n = _ws(ws)
+    _check(lib().moe_layer_decode(ctypes.byref(desc), ctypes.byref(weights), _byref(lora), _ptr(adapter_of_token),
+                                  _ptr(x), _ptr(y), _ptr(topk_idx), _ptr(topk_w), _ptr(counts), p, n,
+                                  _stream(stream)), "moe_layer_decode")
+
+
+def moe_lora_workspace_size(desc: MoeDesc, lora: MoeLora) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_lora_workspace_size(ctypes.byref(desc), _byref(lora), ctypes.byref(n)),
+           "moe_lora_workspace_size")
+    return int(n.value)
+
+
+def moe_grouped_ffn_lora(desc, weights, lora, adapter_of_token, x_perm, offsets, token_of_row, x, y_perm, ws,
+                         stream=None):
+    p, n = _ws(ws)
+    _check(lib().moe_grouped_ffn_lora(ctypes.byref(desc), ctypes.byref(weights), _byref(lora), _ptr(adapter_of_token),
+                                      _ptr(x_perm), _ptr(offsets), _ptr(token_of_row), _ptr(x), _ptr(y_perm), p, n,
+                                      _stream(stream)), "moe_grouped_ffn_lora")
+
+
+def moe_layer_forward_lora(desc, weights, lora, adapter_of_token, x, y, topk_idx, topk_w, counts, ws, stream=None):
+    p, n = _ws(ws)
+    _check(lib().moe_layer_forward_lora(ctypes.byref(desc), ctypes.byref(weights), _byref(lora),
+                                        _ptr(adapter_of_token), _ptr(x), _ptr(y), _ptr(topk_idx), _ptr(topk_w),
+                                        _ptr(counts), p, n, _stream(stream)), "moe_layer_forward_lora")
 
 
 def moe_load_stats(desc, counts, stats, stream=None):
