@@ -5,16 +5,50 @@
 // jsqmd.com "第11章 MoE模型推理" 11.1.1: y = sum_{i in TopK} g_i(x) E_i(x).
 // With a handful of tokens the layer is bound by reading the touched experts'
 // weights once, and a chain of kernels leaves HBM idle at every boundary.
-// Here the steps are phases of one grid, separated by grid barriers:
+// Here the steps are phases of one grid:
 //   route    logits, a warp per (expert, 8 tokens); with E4M3 weights also the
-//            tokens' row codes; then every CTA selects all tokens by itself
-//            and builds the expert groups in shared memory (no barrier)
-//   adapt    (adapters) u = A x of every (token, expert) row
-//   up       hidden = act(x W_in), a warp per (expert, column)
-//   down     y = sum_k g_k hidden_k W_out, a warp per column
+//            tokens' row codes; grid barrier; then every CTA selects all
+//            tokens by itself and builds the expert groups in shared memory
+//   up       hidden = act(x W_in)
+//   down     y = sum_k g_k hidden_k W_out
+//
+// The two products run on the 5th-generation tensor cores with the WEIGHTS as
+// the M = 128 operand and a group's tokens as the N = 16 .. 128 columns, so no
+// row of the product is padding and a weight byte goes HBM -> shared memory
+// -> tensor core without passing through registers.  A step is one 128-byte
+// swizzle row of K (64 bf16 or 128 E4M3) of two 128-row weight tiles that share
+// one token tile: gate and up rows of the same 128 hidden columns (SwiGLU), or
+// 256 neighbouring output columns.  All steps of a phase, in the order (group,
+// tile, k) for up and (tile, group, k) for down, are cut into one equal range
+// per CTA, so every SM reads the same bytes whatever the group sizes are; a
+// tile cut by a range border is joined through fp32 partial sums in the
+// workspace by whichever CTA arrives last, always in CTA order.
+//
+// Roles (384 threads): warp 0 feeds a ring of stages by TMA (the tokens by
+// 4-row gathers straight from x), warp 1 issues the MMAs, warps 4 - 11 are the
+// epilogue, two per TMEM lane quarter.  The weights of the down phase do not
+// depend on the hidden rows, so the producer fills the whole ring with them
+// while the up phase drains and the grid waits for the last hidden row.
+//
+// E4M3 weights: the tokens' codes (one or two per element, see quant.cu) are
+// separate columns of the same product, added in the epilogue.  The codes of a
+// hidden row need the row's maximum: it is kept by integer atomics (order does
+// not matter) while the up phase stores the bf16 hidden rows, and the epilogue
+// warps write the codes between the phases.
+//
+// Adapters: the epilogue warps take the inner products u = A x while the
+// tensor cores start on the up phase (and A hidden at the start of the down
+// phase), and add scale * B u where a tile's sums are final.
+//
+// Every wait is bounded: a CTA that gives up reports MOE_STATUS_TIMEOUT, lets
+// its copies and MMAs in flight finish, frees its TMEM and leaves; the others'
+// waits then run out too.
 #include <math.h>
 
+#include <atomic>
+
 #include "common.cuh"
+#include "gemm_common.cuh"
 #include "kernels.h"
 #include "route_select.cuh"
 #include "row_coding.cuh"
@@ -29,21 +63,30 @@ using route_detail::warp_sum;
 
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
+constexpr int kEpiWarp0 = 4;  // epilogue warps 4 .. 11
+constexpr int kEpiThreads = kThreads - 32 * kEpiWarp0;
 constexpr int kMaxSlabs = 257;
 constexpr int kRouteTokens = 8;  // tokens per warp of the logits
+constexpr int kMaxStages = 8;
+constexpr int kTileBytes = 128 * 128;  // one weight tile of a step: 128 rows x 128 bytes of K
+constexpr int kAccCols = 256;          // TMEM columns of one accumulator pair (128 per tile), two pairs
+constexpr int kTmemCols = 512;
+constexpr size_t kSmemLimit = 232448;  // 227 KB per CTA
 
-// Grid barrier state, in the workspace's first 256 bytes behind the status
-// block.  `arrived` counts arrivals within one call; the last CTA to leave
-// the kernel sets both words back to zero.
+// Grid-wide arrival counters, in the workspace's first 256 bytes behind the
+// status block: they count up within one call; the last CTA to leave the
+// kernel sets them back to zero.
+enum Arrival { kRouted = 0, kInnerUp = 1, kHidden = 2, kCoded = 3, kNumArrivals = 4 };
 struct GridSync {
-  uint32_t arrived;
+  uint32_t arrived[kNumArrivals];
   uint32_t left;
 };
 constexpr size_t kSyncOffset = 128;
-static_assert(sizeof(StatusBlock) <= kSyncOffset, "the grid barrier sits behind the status block");
+static_assert(sizeof(StatusBlock) <= kSyncOffset, "the arrival counters sit behind the status block");
+static_assert(kSyncOffset + sizeof(GridSync) <= 256, "the arrival counters sit in the initialised block");
 
 struct Ws {
-  size_t logits, xq, xs, hidden, hq, hs, u_in, u_out, total;
+  size_t logits, xq, xs, hidden, amax, hq, hs, u_in, u_out, joins, partial, total;
 };
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -61,10 +104,14 @@ Ws ws_layout(int S, int d, int E, int K, int h, int ns, int terms, int rank) {
   L.xq = take(static_cast<size_t>(terms) * S * d);
   L.xs = take(terms ? static_cast<size_t>(S) * 4 : 0);
   L.hidden = take(rows * h * 2);
+  L.amax = take(terms ? rows * 4 : 0);
   L.hq = take(static_cast<size_t>(terms) * rows * h);
   L.hs = take(terms ? rows * 4 : 0);
   L.u_in = take(rows * 2 * rank * 4);
   L.u_out = take(rows * rank * 4);
+  // per CTA: a counter of its first cut tile for each phase, and two tiles' partial sums
+  L.joins = take(2 * kDecodeMaxCtas * 4);
+  L.partial = take(static_cast<size_t>(kDecodeMaxCtas) * 2 * S * 256 * 4);
   L.total = o;
   return L;
 }
@@ -75,26 +122,50 @@ struct Params {
   uint8_t* xq;
   float* xs;
   __nv_bfloat16* hidden;
+  uint32_t* amax;
   uint8_t* hq;
   float* hs;
   float* u_in;
   float* u_out;
+  uint32_t* joins;
+  float* partial;
   StatusBlock* status;
   GridSync* sync;
+  int stages, stage_bytes, ring_bytes;
 };
 
-// Shared-memory tables of one CTA: the selection and the expert groups.
-struct Tables {
-  int idx[MOE_DECODE_MAX_TOKENS * 32];        // [S][K]
-  float gate[MOE_DECODE_MAX_TOKENS * 32];     // [S][K]
-  uint16_t row_slot[MOE_DECODE_MAX_TOKENS * 33];  // row -> slot t*K + k (shared rows: token)
-  int first[kMaxSlabs + 1];                   // active group -> its first row
-  int slab[kMaxSlabs];                        // active group -> weight slab
-  int adapter[MOE_DECODE_MAX_TOKENS];         // token -> adapter or -1
-  int warp_sums[kWarps];
-  int active;
+// Shared-memory control block of one CTA; the selection's arrays follow it.
+struct Ctl {
+  uint64_t full_w[kMaxStages];
+  uint64_t full_b[kMaxStages];
+  uint64_t empty[kMaxStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
   int abort;
+  int active;
+  int last;
+  int warp_sums[kWarps];
+  int first[kMaxSlabs + 1];            // active group -> its first row
+  int slab[kMaxSlabs];                 // active group -> weight slab
+  int adapter[MOE_DECODE_MAX_TOKENS];  // token -> adapter or -1
 };
+
+struct Tables {
+  Ctl* c;
+  float* gate;         // [S][K]
+  int* idx;            // [S][K]
+  uint16_t* row_slot;  // row -> slot t*K + k (shared rows: token)
+  float* y;            // [S][256]: the down phase's sums of one tile, column n owned by one thread
+};
+
+size_t tables_bytes(int S, int K, int ns) {
+  size_t b = (sizeof(Ctl) + 15) & ~size_t(15);
+  b += static_cast<size_t>(S) * K * 8;
+  b += (static_cast<size_t>(S) * (K + ns) * 2 + 15) & ~size_t(15);
+  return b + static_cast<size_t>(S) * 256 * 4;
+}
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
   uint32_t v;
@@ -102,83 +173,125 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
   return v;
 }
 
-// Every CTA of the grid arrives; false when the wait gave up.
-__device__ bool grid_barrier(const Params& p, Tables& t, uint32_t phase) {
+// One thread: wait until every CTA has arrived at `k`.
+__device__ bool wait_arrivals(const Params& p, Arrival k, volatile int* abort_flag) {
+  const uint32_t* word = &p.sync->arrived[k];
+  if (ld_acquire(word) >= gridDim.x) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (ld_acquire(word) < gridDim.x) {
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+  }
+  return true;
+}
+
+__device__ __forceinline__ void give_up(const Params& p, volatile int* abort_flag) {
+  *abort_flag = 1;
+  report(p.status, MOE_STATUS_TIMEOUT, MOE_CNT_TIMEOUT);
+}
+
+// The epilogue warps' barrier; true when any of them passes `failed`.  Its
+// answer is the same for all, so they leave a loop together or not at all.
+__device__ __forceinline__ bool epi_any(bool failed) {
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(static_cast<int>(failed)), "n"(kEpiThreads)
+      : "memory");
+  return any != 0;
+}
+
+// The epilogue warps arrive at `k` for their CTA once their writes are done
+// (written by the generic proxy, read by other CTAs through either).
+__device__ __forceinline__ void epi_arrive(const Params& p, Arrival k) {
+  fence_proxy_async_global();
+  __threadfence();
+  epi_any(false);
+  if (threadIdx.x == 32 * kEpiWarp0) {
+    __threadfence();
+    atomicAdd(&p.sync->arrived[k], 1);
+  }
+}
+
+// The epilogue warps wait for `k`; false (for all of them) when it gave up.
+__device__ __forceinline__ bool epi_wait(const Params& p, Arrival k, volatile int* abort_flag) {
+  bool failed = false;
+  if (threadIdx.x == 32 * kEpiWarp0 && !wait_arrivals(p, k, abort_flag)) {
+    give_up(p, abort_flag);
+    failed = true;
+  }
+  return !epi_any(failed);
+}
+
+// Every thread of every CTA: false when the wait gave up.
+__device__ bool grid_barrier(const Params& p, Ctl& c, Arrival k) {
+  fence_proxy_async_global();
+  __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    atomicAdd(&p.sync->arrived, 1);
-    const uint32_t want = phase * gridDim.x;
-    if (ld_acquire(&p.sync->arrived) < want) {
-      const uint64_t t0 = globaltimer_ns();
-      while (ld_acquire(&p.sync->arrived) < want) {
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-          t.abort = 1;
-          report(p.status, MOE_STATUS_TIMEOUT, MOE_CNT_TIMEOUT);
-          break;
-        }
-      }
-    }
+    atomicAdd(&p.sync->arrived[k], 1);
+    if (!wait_arrivals(p, k, &c.abort)) give_up(p, &c.abort);
   }
   __syncthreads();
-  return t.abort == 0;
+  fence_proxy_async_global();
+  return c.abort == 0;
 }
 
+// The last CTA to leave sets the counters back for the next call.
 __device__ void leave(const Params& p) {
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
     if (atomicAdd(&p.sync->left, 1) == gridDim.x - 1) {
-      p.sync->arrived = 0;
+      for (int i = 0; i < kNumArrivals; ++i) p.sync->arrived[i] = 0;
       p.sync->left = 0;
     }
   }
 }
 
-__device__ __forceinline__ float e4m3_value(uint32_t c) {
-  const float m = coding::e4m3_magnitude(c);
-  return (c & 0x80u) ? -m : m;
-}
-
-// Sum over a warp of w[k] * row[k] for one weight row: bf16 operands, or E4M3
-// weight codes against the row's one or two terms.
-__device__ float warp_dot(const void* w, const void* row, int n, int terms) {
+// Sum over a warp of the products of two bf16 rows; `row` may have been
+// written by this grid, so it is read at L2.
+__device__ float warp_dot(const __nv_bfloat16* w, const __nv_bfloat16* row, int n) {
   float acc = 0.0f;
-  const int lane = lane_id();
-  if (terms == 0) {
-    for (int c = lane * 8; c < n; c += 256) {
-      float a[8], b[8];
-      coding::bf16x8_to_f32(ldg16(static_cast<const __nv_bfloat16*>(w) + c), a);
-      coding::bf16x8_to_f32(__ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(row) + c)), b);
+  for (int c = lane_id() * 8; c < n; c += 256) {
+    float a[8], b[8];
+    coding::bf16x8_to_f32(ldg16(w + c), a);
+    coding::bf16x8_to_f32(__ldcg(reinterpret_cast<const uint4*>(row + c)), b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc = fmaf(a[j], b[j], acc);
-    }
-  } else {
-    const auto* wc = static_cast<const uint8_t*>(w);
-    const auto* rc = static_cast<const uint8_t*>(row);
-    for (int c = lane * 4; c < n; c += 128) {
-      const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(wc + c));
-      const uint32_t r1 = __ldcg(reinterpret_cast<const uint32_t*>(rc + c));
-      const uint32_t r2 = terms == 2 ? __ldcg(reinterpret_cast<const uint32_t*>(rc + n + c)) : 0u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc = fmaf(e4m3_value(q >> (8 * j)), e4m3_value(r1 >> (8 * j)) + e4m3_value(r2 >> (8 * j)), acc);
-    }
+    for (int j = 0; j < 8; ++j) acc = fmaf(a[j], b[j], acc);
   }
   return warp_sum(acc);
 }
 
-// scale * sum_r u[r] B[a][slab][n][r], by a warp.
-__device__ float warp_delta(const LoraParams& l, int m, int slabs, int a, int slab, int out, int n, const float* u) {
+// scale * sum_r u[r] B[a][slab][n][r], by one thread.
+__device__ float adapter_delta(const LoraParams& l, int m, int slabs, int a, int slab, int out, int n, const float* u) {
   const auto* b = static_cast<const __nv_bfloat16*>(l.b[m]) +
                   ((static_cast<int64_t>(a) * slabs + slab) * out + n) * l.r;
   float acc = 0.0f;
-  for (int i = lane_id(); i < l.r; i += 32) acc = fmaf(to_f32(b[i]), __ldcg(u + i), acc);
-  return warp_sum(acc) * __ldg(l.scale + a);
+  for (int i = 0; i < l.r; i += 8) {
+    float bf[8];
+    coding::bf16x8_to_f32(ldg16(b + i), bf);
+    const float4 u0 = __ldcg(reinterpret_cast<const float4*>(u + i));
+    const float4 u1 = __ldcg(reinterpret_cast<const float4*>(u + i + 4));
+    acc = fmaf(bf[0], u0.x, acc);
+    acc = fmaf(bf[1], u0.y, acc);
+    acc = fmaf(bf[2], u0.z, acc);
+    acc = fmaf(bf[3], u0.w, acc);
+    acc = fmaf(bf[4], u1.x, acc);
+    acc = fmaf(bf[5], u1.y, acc);
+    acc = fmaf(bf[6], u1.z, acc);
+    acc = fmaf(bf[7], u1.w, acc);
+  }
+  return acc * __ldg(l.scale + a);
 }
 
 template <int NI>
-__device__ void select_tokens(const Params& p, Tables& t, const SelectParams& sp) {
+__device__ void select_tokens(const Params& p, const SelectParams& sp) {
   const int warp = threadIdx.x >> 5, lane = lane_id();
   for (int tok = warp; tok < p.a.S; tok += kWarps) {
     float l[NI];
@@ -191,9 +304,16 @@ __device__ void select_tokens(const Params& p, Tables& t, const SelectParams& sp
   }
 }
 
-// Router logits and, with E4M3 weights, the tokens' codes.
+// Router logits and, with E4M3 weights, the tokens' codes; the join counters
+// and row maxima of this call start at zero.
 __device__ void route_phase(const Params& p) {
   const DecodeArgs& a = p.a;
+  const int rows = a.S * (a.K + a.num_shared);
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < 2 * kDecodeMaxCtas || (a.terms && i < rows);
+       i += gridDim.x * kThreads) {
+    if (i < 2 * kDecodeMaxCtas) p.joins[i] = 0;
+    if (a.terms && i < rows) p.amax[i] = 0;
+  }
   const int warp = threadIdx.x >> 5, lane = lane_id();
   const int tb = (a.S + kRouteTokens - 1) / kRouteTokens;
   const int dots = a.E * tb, items = dots + (a.terms ? a.S : 0);
@@ -233,19 +353,19 @@ __device__ void route_phase(const Params& p) {
 }
 
 // Selection of every token and the group tables, by each CTA for itself.
-__device__ void tables_phase(const Params& p, Tables& t) {
+__device__ void tables_phase(const Params& p, const Tables& t) {
   const DecodeArgs& a = p.a;
   const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
   SelectParams sp{a.E,        a.K,    a.score_fn, a.renormalize, a.num_groups, a.topk_groups, a.tau,
                   a.sel_bias, t.idx,  t.gate,     blockIdx.x == 0 ? p.status : nullptr, nullptr, nullptr};
   if (a.E <= 32)
-    select_tokens<1>(p, t, sp);
+    select_tokens<1>(p, sp);
   else if (a.E <= 64)
-    select_tokens<2>(p, t, sp);
+    select_tokens<2>(p, sp);
   else if (a.E <= 128)
-    select_tokens<4>(p, t, sp);
+    select_tokens<4>(p, sp);
   else
-    select_tokens<8>(p, t, sp);
+    select_tokens<8>(p, sp);
   if (a.lora.n > 0) {
     for (int i = tid; i < a.S; i += kThreads) {
       int id = __ldg(a.lora.ids + i);
@@ -253,7 +373,7 @@ __device__ void tables_phase(const Params& p, Tables& t) {
         if (blockIdx.x == 0) report(p.status, MOE_STATUS_BAD_ADAPTER, -1);
         id = -1;
       }
-      t.adapter[i] = id;
+      t.c->adapter[i] = id;
     }
   }
   __syncthreads();
@@ -273,14 +393,14 @@ __device__ void tables_phase(const Params& p, Tables& t) {
     const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
     if (lane >= off) incl += o;
   }
-  if (lane == 31) t.warp_sums[warp] = incl;
+  if (lane == 31) t.c->warp_sums[warp] = incl;
   __syncthreads();
   int before = incl - v;
-  for (int w = 0; w < warp; ++w) before += t.warp_sums[w];
+  for (int w = 0; w < warp; ++w) before += t.c->warp_sums[w];
   const int row0 = before & 0xFFFF, group = before >> 16;
   if (tid < slabs && count > 0) {
-    t.first[group] = row0;
-    t.slab[group] = tid;
+    t.c->first[group] = row0;
+    t.c->slab[group] = tid;
     if (tid < a.E) {
       int r = row0;
       for (int i = 0; i < slots; ++i)
@@ -291,8 +411,8 @@ __device__ void tables_phase(const Params& p, Tables& t) {
   }
   if (tid == kThreads - 1) {
     const int all = before + v;
-    t.active = all >> 16;
-    t.first[all >> 16] = all & 0xFFFF;
+    t.c->active = all >> 16;
+    t.c->first[all >> 16] = all & 0xFFFF;
   }
   if (blockIdx.x == 0) {
     if (a.counts != nullptr && tid < a.E) a.counts[tid] = count;
@@ -309,32 +429,18 @@ struct Row {
   float gate;
 };
 
-// Codes of one hidden row by a warp.  The row was written by this grid, so it
-// is read at L2 (ld.global.cg), twice: maximum, then codes.
-__device__ void code_hidden_row(const __nv_bfloat16* src, uint8_t* dst, float* scale, int n, int terms) {
-  const int lane = lane_id();
-  uint32_t acc = 0;
-  for (int c = lane * 8; c < n; c += 256) acc = coding::absmax_bits8(acc, __ldcg(reinterpret_cast<const uint4*>(src + c)));
-  const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, max(acc & 0xFFFFu, acc >> 16));
-  float s, m;
-  coding::row_scale(terms, __uint_as_float(bits << 16), bits > 0x7F80u, bits >= 0x7F80u, s, m);
-  for (int c = lane * 8; c < n; c += 256)
-    coding::code_piece(__ldcg(reinterpret_cast<const uint4*>(src + c)), dst, n, c, terms, s, m);
-  if (lane == 0) *scale = s;
-}
-
-// The row `r` of the active group with slab `slab`.
+// The row `r` of an active group with slab `slab`.
 __device__ __forceinline__ Row row_at(const Params& p, const Tables& t, int slab, int r) {
   const int s = t.row_slot[r];
   if (slab == p.a.E) return Row{s, 1.0f};
   return Row{s / p.a.K, t.gate[s]};
 }
 
-__device__ __forceinline__ int group_of_row(const Tables& t, int r) {
-  int lo = 0, hi = t.active;
+__device__ __forceinline__ int group_of_row(const Ctl& c, int r) {
+  int lo = 0, hi = c.active;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (t.first[mid] <= r)
+    if (c.first[mid] <= r)
       lo = mid;
     else
       hi = mid;
@@ -342,121 +448,612 @@ __device__ __forceinline__ int group_of_row(const Tables& t, int r) {
   return lo;
 }
 
-// u[row][m][i] = A_m[a][slab][i] . row for the pairs m0 .. m0 + nm - 1.
+// Epilogue warps: u[row][m][i] = A_m[a][slab][i] . row for the pairs m0 .. m0 + nm - 1.
 __device__ void adapter_inner(const Params& p, const Tables& t, int m0, int nm) {
   const LoraParams& l = p.a.lora;
-  const int rows = t.first[t.active], slabs = p.a.E + p.a.num_shared;
-  const int warp = threadIdx.x >> 5;
+  const int rows = t.c->first[t.c->active], slabs = p.a.E + p.a.num_shared;
+  const int warp = (threadIdx.x >> 5) - kEpiWarp0;
   const int n = m0 == 2 ? p.a.h : p.a.d;
   float* out = m0 == 2 ? p.u_out : p.u_in;
-  for (int i = blockIdx.x + gridDim.x * warp; i < rows * nm * l.r; i += gridDim.x * kWarps) {
+  for (int i = blockIdx.x + gridDim.x * warp; i < rows * nm * l.r; i += gridDim.x * (kEpiThreads / 32)) {
     const int j = i % l.r, m = m0 + (i / l.r) % nm, r = i / (l.r * nm);
     if (l.a[m] == nullptr) continue;
-    const int slab = t.slab[group_of_row(t, r)];
-    const int token = row_at(p, t, slab, r).token, ad = t.adapter[token];
+    const int slab = t.c->slab[group_of_row(*t.c, r)];
+    const int token = row_at(p, t, slab, r).token, ad = t.c->adapter[token];
     if (ad < 0) continue;
     const auto* w = static_cast<const __nv_bfloat16*>(l.a[m]) + ((static_cast<int64_t>(ad) * slabs + slab) * l.r + j) * n;
     const __nv_bfloat16* src = m0 == 2 ? p.hidden + static_cast<int64_t>(r) * n
                                        : static_cast<const __nv_bfloat16*>(p.a.x) + static_cast<int64_t>(token) * n;
-    const float v = warp_dot(w, src, n, 0);
+    const float v = warp_dot(w, src, n);
     if (lane_id() == 0) out[(static_cast<int64_t>(r) * nm + (m - m0)) * l.r + j] = v;
   }
 }
 
-__device__ void up_phase(const Params& p, const Tables& t) {
+// Epilogue warps: the hidden rows' codes from their maxima, a warp per 1024 columns of a row.
+__device__ void code_hidden(const Params& p, const Tables& t) {
   const DecodeArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, slabs = a.E + a.num_shared;
-  const int wb = a.terms ? 1 : 2;
-  const bool swiglu = a.activation == MOE_ACT_SWIGLU;
-  for (int64_t i = blockIdx.x + gridDim.x * warp; i < static_cast<int64_t>(t.active) * a.h; i += gridDim.x * kWarps) {
-    const int g = static_cast<int>(i / a.h), n = static_cast<int>(i % a.h), slab = t.slab[g];
-    const int64_t ch = static_cast<int64_t>(slab) * a.h + n;
-    for (int r = t.first[g]; r < t.first[g + 1]; ++r) {
-      const int token = row_at(p, t, slab, r).token;
-      const void* src = a.terms ? static_cast<const void*>(p.xq + static_cast<int64_t>(token) * a.terms * a.d)
-                                : static_cast<const void*>(static_cast<const __nv_bfloat16*>(a.x) +
-                                                           static_cast<int64_t>(token) * a.d);
-      const float rs = a.terms ? __ldcg(p.xs + token) : 1.0f;
-      float v[2] = {0.0f, 0.0f};
-      for (int m = swiglu ? 0 : 1; m < 2; ++m) {
-        const int q = swiglu ? m : 0;
-        v[m] = rs * warp_dot(static_cast<const char*>(a.w_in[q]) + ch * a.d * wb, src, a.d, a.terms);
-        if (a.terms) v[m] *= __ldg(a.s_in[q] + ch);
-        if (a.lora.n > 0 && a.lora.a[m] != nullptr && t.adapter[token] >= 0)
-          v[m] += warp_delta(a.lora, m, slabs, t.adapter[token], slab, a.h, n,
-                             p.u_in + (static_cast<int64_t>(r) * 2 + m) * a.lora.r);
-      }
-      float out;
-      if (swiglu) {
-        out = v[0] / (1.0f + __expf(-v[0])) * v[1];
-      } else {
-        const float z = v[1] + __ldg(a.b_in + ch);
-        out = 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-      }
-      if (lane_id() == 0) p.hidden[static_cast<int64_t>(r) * a.h + n] = __float2bfloat16_rn(out);
-    }
-  }
-}
-
-__device__ void down_phase(const Params& p, const Tables& t) {
-  const DecodeArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = lane_id(), slabs = a.E + a.num_shared;
-  const int wb = a.terms ? 1 : 2;
-  auto* y = static_cast<__nv_bfloat16*>(a.y);
-  for (int n = blockIdx.x + gridDim.x * warp; n < a.d; n += gridDim.x * kWarps) {
-    float acc[2] = {0.0f, 0.0f};  // tokens lane, lane + 32
-    for (int g = 0; g < t.active; ++g) {
-      const int slab = t.slab[g];
-      const int64_t ch = static_cast<int64_t>(slab) * a.d + n;
-      for (int r = t.first[g]; r < t.first[g + 1]; ++r) {
-        const Row row = row_at(p, t, slab, r);
-        const void* src = a.terms ? static_cast<const void*>(p.hq + static_cast<int64_t>(r) * a.terms * a.h)
-                                  : static_cast<const void*>(p.hidden + static_cast<int64_t>(r) * a.h);
-        float v = warp_dot(static_cast<const char*>(a.w_out) + ch * a.h * wb, src, a.h, a.terms);
-        if (a.terms) v *= __ldcg(p.hs + r) * __ldg(a.s_out + ch);
-        if (a.lora.n > 0 && a.lora.a[2] != nullptr && t.adapter[row.token] >= 0)
-          v += warp_delta(a.lora, 2, slabs, t.adapter[row.token], slab, a.d, n,
-                          p.u_out + static_cast<int64_t>(r) * a.lora.r);
-        if (a.b_out != nullptr) v += __ldg(a.b_out + ch);
-        if ((row.token & 31) == lane) acc[row.token >> 5] += row.gate * v;
-      }
-    }
+  const int rows = t.c->first[t.c->active], pieces = (a.h + 1023) / 1024;
+  const int warp = (threadIdx.x >> 5) - kEpiWarp0;
+  for (int i = blockIdx.x + gridDim.x * warp; i < rows * pieces; i += gridDim.x * (kEpiThreads / 32)) {
+    const int r = i / pieces, c0 = (i % pieces) * 1024 + lane_id() * 8;
+    const uint32_t bits = __ldcg(p.amax + r);
+    float s, m;
+    coding::row_scale(a.terms, __uint_as_float(bits << 16), bits > 0x7F80u, bits >= 0x7F80u, s, m);
+    const __nv_bfloat16* src = p.hidden + static_cast<int64_t>(r) * a.h;
+    uint8_t* dst = p.hq + static_cast<int64_t>(r) * a.terms * a.h;
+    uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (lane + 32 * i < a.S) y[static_cast<int64_t>(lane + 32 * i) * a.d + n] = __float2bfloat16_rn(acc[i]);
+    for (int k = 0; k < 4; ++k)
+      v[k] = c0 + 256 * k < a.h ? __ldcg(reinterpret_cast<const uint4*>(src + c0 + 256 * k)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c0 + 256 * k < a.h) coding::code_piece(v[k], dst, a.h, c0 + 256 * k, a.terms, s, m);
+    if (i % pieces == 0 && lane_id() == 0) p.hs[r] = s;
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Params p) {
-  extern __shared__ uint8_t smem[];
-  Tables& t = *reinterpret_cast<Tables*>(smem);
+// The steps of one phase and this CTA's range of them.  Unit: the part of one
+// tile that lies in the range.
+struct Phase {
+  int nk;         // steps of a tile (its K)
+  int64_t lo, hi; // this CTA's steps
+  int64_t total;
+  int parts;      // CTAs that have steps: every one of them at least one
+};
+
+__device__ __forceinline__ Phase phase_of(int tiles, int nk) {
+  Phase f;
+  f.nk = nk;
+  f.total = static_cast<int64_t>(tiles) * nk;
+  f.parts = f.total < gridDim.x ? static_cast<int>(f.total) : static_cast<int>(gridDim.x);
+  const int c = static_cast<int>(blockIdx.x);
+  f.lo = c < f.parts ? f.total * c / f.parts : f.total;
+  f.hi = c < f.parts ? f.total * (c + 1) / f.parts : f.total;
+  return f;
+}
+
+struct Unit {
+  int tile, k0, k1;
+};
+
+__device__ __forceinline__ Unit unit_at(const Phase& f, int64_t s) {
+  Unit u;
+  u.tile = static_cast<int>(s / f.nk);
+  u.k0 = static_cast<int>(s - static_cast<int64_t>(u.tile) * f.nk);
+  const int64_t left = f.hi - s;
+  u.k1 = left < f.nk - u.k0 ? u.k0 + static_cast<int>(left) : f.nk;
+  return u;
+}
+
+// A tile that several CTAs share: the CTAs c0 .. c1 hold its steps from s0 on,
+// each with a partial tile of its own, element [tok][half * 128 + n].
+struct Join {
+  int c0, c1;
+  int64_t s0, total;
+  int parts;
+};
+
+__device__ __forceinline__ Join join_of(const Phase& f, int64_t s0, int64_t s1) {
+  // the CTA of step s: the largest c with floor(total c / parts) <= s, i.e. c < (s + 1) parts / total
+  return Join{static_cast<int>(((s0 + 1) * f.parts - 1) / f.total), static_cast<int>((s1 * f.parts - 1) / f.total), s0,
+              f.total, f.parts};
+}
+
+// Partial tile of CTA c: 0 for a tile that began before its range, else 1.
+__device__ __forceinline__ float* partial_of(const Params& p, const Join& j, int c) {
+  const int64_t lo = j.total * c / j.parts;
+  return p.partial + (static_cast<int64_t>(c) * 2 + (lo > j.s0 ? 0 : 1)) * p.a.S * 256;
+}
+
+__device__ __forceinline__ float join_sum(const Params& p, const Join& j, int at) {
+  float v = 0.0f;
+  for (int c = j.c0; c <= j.c1; ++c) v += __ldcg(partial_of(p, j, c) + at);
+  return v;
+}
+
+// The epilogue warps have written this CTA's part: true for all of them when
+// it was the last one.
+__device__ __forceinline__ bool join_last(const Params& p, const Tables& t, const Join& j, int phase) {
+  __threadfence();
+  epi_any(false);
+  if (threadIdx.x == 32 * kEpiWarp0) {
+    __threadfence();
+    t.c->last = atomicAdd(p.joins + phase * kDecodeMaxCtas + j.c0, 1) == static_cast<uint32_t>(j.c1 - j.c0);
+  }
+  epi_any(false);
+  const bool last = t.c->last != 0;
+  __threadfence();
+  return last;
+}
+
+// Ring position: stage and how often the ring has gone round.
+struct Slot {
+  int stage = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      round ^= 1;
+    }
+  }
+};
+
+// Output rows of one group's tile: which weight rows, which token rows.
+struct Maps {
+  const CUtensorMap *w0, *w1, *x, *hidden;
+};
+
+// Warp 0.  Weight tiles and token tiles have barriers of their own, so a stage's
+// weights can be under way before its tokens exist.
+struct Producer {
+  const Params& p;
+  const Tables& t;
+  uint8_t* ring;
+  Slot w, b;
+  uint32_t armed_w = 0, armed_b = 0, round_w = 0, round_b = 0;  // barriers armed, for an abort
+
+  __device__ Producer(const Params& p_, const Tables& t_, uint8_t* ring_) : p(p_), t(t_), ring(ring_) {}
+
+  // Two weight tiles: rows n0 of slab `slab` of w0, and rows n1 of w1.
+  __device__ bool weights(const CUtensorMap* w0, const CUtensorMap* w1, int k, int n0, int n1, int slab) {
+    const int lane = lane_id();
+    Ctl& c = *t.c;
+    bool ok = true;
+    if (lane == 0) ok = mbar_wait(&c.empty[w.stage], w.round ^ 1u, &c.abort);
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    if (!ok) return false;
+    uint8_t* st = ring + w.stage * p.stage_bytes;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&c.full_w[w.stage], 2 * kTileBytes);
+      tma_load_3d(st, w0, k, n0, slab, &c.full_w[w.stage]);
+      tma_load_3d(st + kTileBytes, w1, k, n1, slab, &c.full_w[w.stage]);
+    }
+    armed_w |= 1u << w.stage;
+    round_w = (round_w & ~(1u << w.stage)) | (w.round << w.stage);
+    w.next(p.stages);
+    return true;
+  }
+
+  // Token tile of the up phase: the group's tokens, `terms` columns each.
+  __device__ void tokens(const CUtensorMap* m, int k, int row0, int n) {
+    const int lane = lane_id();
+    Ctl& c = *t.c;
+    const int terms = p.a.terms == 2 ? 2 : 1, cols = n * terms, quads = (cols + 3) / 4;
+    uint8_t* dst = ring + b.stage * p.stage_bytes + 2 * kTileBytes;
+    if (lane == 0) mbar_arrive_expect_tx(&c.full_b[b.stage], quads * 512);
+    __syncwarp();
+    if (lane < quads) {
+      int r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = min(4 * lane + i, cols - 1);  // past the group: its last column again
+        const int tok = token_of(row0 + col / terms);
+        r[i] = tok * terms + col % terms;
+      }
+      tma_gather4(dst + lane * 512, m, k, r[0], r[1], r[2], r[3], &c.full_b[b.stage]);
+    }
+    arm_b();
+  }
+
+  // Token tile of the down phase: the group's hidden rows, in boxes of 16.
+  __device__ void hidden(const CUtensorMap* m, int k, int row0, int n) {
+    const int lane = lane_id();
+    Ctl& c = *t.c;
+    const int terms = p.a.terms == 2 ? 2 : 1, boxes = (n * terms + 15) / 16;
+    uint8_t* dst = ring + b.stage * p.stage_bytes + 2 * kTileBytes;
+    if (lane == 0) mbar_arrive_expect_tx(&c.full_b[b.stage], boxes * 2048);
+    __syncwarp();
+    if (lane < boxes) tma_load_2d(dst + lane * 2048, m, k, row0 * terms + 16 * lane, &c.full_b[b.stage]);
+    arm_b();
+  }
+
+  __device__ __forceinline__ int token_of(int r) const {
+    const int s = t.row_slot[r];
+    return r >= p.a.S * p.a.K ? s : s / p.a.K;
+  }
+
+  __device__ __forceinline__ void arm_b() {
+    armed_b |= 1u << b.stage;
+    round_b = (round_b & ~(1u << b.stage)) | (b.round << b.stage);
+    b.next(p.stages);
+  }
+
+  // Lets every copy in flight land (each barrier's last armed round).
+  __device__ void settle() {
+    if (lane_id() != 0) return;
+    int never = 0;
+    for (int i = 0; i < p.stages; ++i) {
+      if (armed_w & (1u << i)) mbar_wait(&t.c->full_w[i], (round_w >> i) & 1u, &never);
+      if (armed_b & (1u << i)) mbar_wait(&t.c->full_b[i], (round_b >> i) & 1u, &never);
+    }
+  }
+};
+
+__device__ void produce(const Params& p, const Tables& t, uint8_t* ring, const Phase& up, const Phase& down,
+                        const Maps& mu, const Maps& md) {
   const DecodeArgs& a = p.a;
-  if (threadIdx.x == 0) t.abort = 0;
-  uint32_t phase = 0;
+  Ctl& c = *t.c;
+  const int bk = a.terms ? 128 : 64;
+  const bool pair = a.activation == MOE_ACT_SWIGLU;
+  const int tiles = (a.h + (pair ? 127 : 255)) / (pair ? 128 : 256);
+  Producer pr(p, t, ring);
+  bool ok = true;
+  for (int64_t s = up.lo; s < up.hi && ok;) {
+    const Unit u = unit_at(up, s);
+    const int g = u.tile / tiles, j = u.tile % tiles, slab = c.slab[g];
+    const int n0 = pair ? j * 128 : j * 256, n1 = pair ? n0 : n0 + 128;
+    for (int k = u.k0; k < u.k1; ++k) {
+      if (!(ok = pr.weights(mu.w0, mu.w1, k * bk, n0, n1, slab))) break;
+      pr.tokens(mu.x, k * bk, c.first[g], c.first[g + 1] - c.first[g]);
+    }
+    s += u.k1 - u.k0;
+  }
+  // down: the first `ahead` steps' weights go out before the hidden rows are known to be complete
+  const int64_t steps = down.hi - down.lo;
+  const int ahead = static_cast<int>(steps < p.stages ? steps : p.stages);
+  auto down_step = [&](int64_t s, bool weights, bool tokens) {
+    const int tile = static_cast<int>(s / down.nk), k = static_cast<int>(s % down.nk);
+    const int j = tile / c.active, g = tile % c.active;
+    if (weights && !pr.weights(md.w0, md.w1, k * bk, j * 256, j * 256 + 128, c.slab[g])) return false;
+    if (tokens) pr.hidden(md.hidden, k * bk, c.first[g], c.first[g + 1] - c.first[g]);
+    return true;
+  };
+  for (int i = 0; i < ahead && ok; ++i) ok = down_step(down.lo + i, true, false);
+  if (ok) {
+    if (lane_id() == 0) ok = wait_arrivals(p, a.terms ? kCoded : kHidden, &c.abort);
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    fence_proxy_async_global();
+  }
+  for (int i = 0; i < ahead && ok; ++i) ok = down_step(down.lo + i, false, true);
+  for (int64_t s = down.lo + ahead; s < down.hi && ok; ++s) ok = down_step(s, true, true);
+  if (!ok) {
+    if (lane_id() == 0) give_up(p, &c.abort);
+    pr.settle();
+  }
+}
+
+// Warp 1, one lane.
+__device__ void multiply(const Params& p, const Tables& t, uint8_t* ring, const Phase& up, const Phase& down) {
+  const DecodeArgs& a = p.a;
+  Ctl& c = *t.c;
+  const bool pair = a.activation == MOE_ACT_SWIGLU;
+  const int tiles = (a.h + (pair ? 127 : 255)) / (pair ? 128 : 256);
+  const int terms = a.terms == 2 ? 2 : 1;
+  Slot at;
+  int local = 0;
+  bool ok = true;
+  for (int ph = 0; ph < 2 && ok; ++ph) {
+    const Phase& f = ph == 0 ? up : down;
+    for (int64_t s = f.lo; s < f.hi && ok; ++local) {
+      const Unit u = unit_at(f, s);
+      const int g = ph == 0 ? u.tile / tiles : u.tile % c.active;
+      const int n = ((c.first[g + 1] - c.first[g]) * terms + 15) & ~15;
+      const uint32_t idesc = a.terms ? idesc_e4m3_f32(128, n) : idesc_bf16_f32(128, n);
+      const int acc = local & 1;
+      if (!(ok = mbar_wait(&c.tempty[acc], ((local >> 1) & 1) ^ 1u, &c.abort))) break;
+      tc_fence_after();
+      const uint32_t d0 = c.tmem_base + acc * kAccCols, d1 = d0 + kAccCols / 2;
+      for (int k = u.k0; k < u.k1; ++k) {
+        if (!(ok = mbar_wait(&c.full_w[at.stage], at.round, &c.abort))) break;
+        if (!(ok = mbar_wait(&c.full_b[at.stage], at.round, &c.abort))) break;
+        tc_fence_after();
+        const uint32_t w = smem_u32(ring + at.stage * p.stage_bytes), b = w + 2 * kTileBytes;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint32_t on = (k > u.k0 || kk > 0) ? 1u : 0u;
+          const uint64_t bd = smem_desc_sw128(b + kk * 32);
+          if (a.terms) {
+            tc_mma_f8(d0, smem_desc_sw128(w + kk * 32), bd, idesc, on);
+            tc_mma_f8(d1, smem_desc_sw128(w + kTileBytes + kk * 32), bd, idesc, on);
+          } else {
+            tc_mma_f16(d0, smem_desc_sw128(w + kk * 32), bd, idesc, on);
+            tc_mma_f16(d1, smem_desc_sw128(w + kTileBytes + kk * 32), bd, idesc, on);
+          }
+        }
+        tc_commit(&c.empty[at.stage]);
+        at.next(p.stages);
+      }
+      if (!ok) break;
+      tc_commit(&c.tfull[acc]);
+      s += u.k1 - u.k0;
+    }
+  }
+  tc_commit(&c.drain);  // every MMA issued must finish before TMEM is released
+  int never = 0;
+  mbar_wait(&c.drain, 0, &never);
+  if (!ok) give_up(p, &c.abort);
+}
+
+// Eight accumulator columns -> the sums of their 8 (or, two terms, 4) tokens.
+__device__ __forceinline__ void load_sums(uint32_t taddr, int terms, float (&v)[8]) {
+  uint32_t r[8];
+  tmem_ld_32x32b_x8(taddr, r);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+  if (terms == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = v[2 * i] + v[2 * i + 1];
+  }
+}
+
+// Final sums of hidden column n of row r (token `tok`): scales, adapters, bias,
+// activation.  v0, v1: gate and up (SwiGLU), or v0 alone.
+__device__ __forceinline__ float hidden_value(const Params& p, const Tables& t, int slab, int r, int tok, int n,
+                                              float v0, float v1) {
+  const DecodeArgs& a = p.a;
+  const int64_t ch = static_cast<int64_t>(slab) * a.h + n;
+  const bool pair = a.activation == MOE_ACT_SWIGLU;
+  if (a.terms) {
+    const float rs = __ldcg(p.xs + tok);
+    v0 *= rs * __ldg(a.s_in[0] + ch);
+    v1 *= rs * __ldg(a.s_in[1] + ch);
+  }
+  if (a.lora.n > 0) {
+    const int ad = t.c->adapter[tok], slabs = a.E + a.num_shared;
+    if (ad >= 0) {
+      const float* u = p.u_in + static_cast<int64_t>(r) * 2 * a.lora.r;
+      if (pair) {
+        if (a.lora.a[0] != nullptr) v0 += adapter_delta(a.lora, 0, slabs, ad, slab, a.h, n, u);
+        if (a.lora.a[1] != nullptr) v1 += adapter_delta(a.lora, 1, slabs, ad, slab, a.h, n, u + a.lora.r);
+      } else if (a.lora.a[1] != nullptr) {
+        v0 += adapter_delta(a.lora, 1, slabs, ad, slab, a.h, n, u + a.lora.r);
+      }
+    }
+  }
+  if (pair) return v0 / (1.0f + __expf(-v0)) * v1;
+  const float z = v0 + __ldg(a.b_in + ch);
+  return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+}
+
+// Store hidden value `v` of (row, n) and, with E4M3 weights, raise the row's
+// maximum (one atomic per warp; lanes past the last column pass in = false).
+__device__ __forceinline__ void store_hidden(const Params& p, int r, int n, bool in, float v) {
+  const __nv_bfloat16 q = __float2bfloat16_rn(v);
+  if (in) p.hidden[static_cast<int64_t>(r) * p.a.h + n] = q;
+  if (p.a.terms) {
+    const uint32_t bits = in ? (__bfloat16_as_ushort(q) & 0x7FFFu) : 0u;
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, bits);
+    if (lane_id() == 0) atomicMax(p.amax + r, m);
+  }
+}
+
+// One hidden element of a tile: tile column `n` (0..127) of half `m`.
+__device__ __forceinline__ int hidden_col(bool pair, int j, int m, int n) { return pair ? j * 128 + n : j * 256 + m * 128 + n; }
+
+__device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, int& local) {
+  const DecodeArgs& a = p.a;
+  Ctl& c = *t.c;
+  const int warp = threadIdx.x >> 5, lane = lane_id(), q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+  const bool pair = a.activation == MOE_ACT_SWIGLU;
+  const int tiles = (a.h + (pair ? 127 : 255)) / (pair ? 128 : 256);
+  const int terms = a.terms == 2 ? 2 : 1, per = 8 / terms;  // tokens per 8 columns
+  const int nl = q * 32 + lane;
+  bool inner_ready = a.lora.n == 0 || (a.lora.a[0] == nullptr && a.lora.a[1] == nullptr);
+  for (int64_t s = f.lo; s < f.hi; ++local) {
+    const Unit u = unit_at(f, s);
+    s += u.k1 - u.k0;
+    const int g = u.tile / tiles, j = u.tile % tiles, slab = c.slab[g];
+    const int row0 = c.first[g], cnt = c.first[g + 1] - row0;
+    const bool whole = u.k0 == 0 && u.k1 == f.nk;
+    const Join jn = join_of(f, static_cast<int64_t>(u.tile) * f.nk, static_cast<int64_t>(u.tile + 1) * f.nk);
+    float* part = partial_of(p, jn, blockIdx.x);
+    if (!inner_ready) {
+      if (!epi_wait(p, kInnerUp, &c.abort)) return false;
+      inner_ready = true;
+    }
+    const int acc = local & 1;
+    bool failed = false;
+    if (!mbar_wait(&c.tfull[acc], (local >> 1) & 1, &c.abort)) {
+      if (lane == 0) give_up(p, &c.abort);
+      failed = true;
+    }
+    if (epi_any(failed)) return false;
+    tc_fence_after();
+    const uint32_t tb = c.tmem_base + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
+    const int chunks = (cnt + per - 1) / per;
+    // SwiGLU: the two halves of the warps take alternate chunks of columns, both tiles; else one tile each
+    for (int ch = pair ? half : 0; ch < chunks; ch += pair ? 2 : 1) {
+      float v0[8], v1[8];
+      load_sums(tb + (pair ? 0 : half * (kAccCols / 2)) + ch * 8, terms, v0);
+      if (pair) load_sums(tb + kAccCols / 2 + ch * 8, terms, v1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int tk = ch * per + i;
+        if (i >= per || tk >= cnt) break;
+        if (!whole) {
+          if (pair) {
+            part[tk * 256 + nl] = v0[i];
+            part[tk * 256 + 128 + nl] = v1[i];
+          } else {
+            part[tk * 256 + half * 128 + nl] = v0[i];
+          }
+          continue;
+        }
+        const int n = hidden_col(pair, j, half, nl), r = row0 + tk;
+        const bool in = n < a.h;
+        const int tok = row_at(p, t, slab, r).token;
+        store_hidden(p, r, n, in, in ? hidden_value(p, t, slab, r, tok, n, v0[i], pair ? v1[i] : 0.0f) : 0.0f);
+      }
+    }
+    tc_fence_before();
+    mbar_arrive(&c.tempty[acc]);
+    if (whole) continue;
+    if (!join_last(p, t, jn, 0)) continue;
+    for (int tk = pair ? half : 0; tk < cnt; tk += pair ? 2 : 1) {
+      const int n = hidden_col(pair, j, half, nl), r = row0 + tk;
+      const bool in = n < a.h;
+      const float s0 = join_sum(p, jn, tk * 256 + (pair ? 0 : half * 128) + nl);
+      const float s1 = pair ? join_sum(p, jn, tk * 256 + 128 + nl) : 0.0f;
+      const int tok = row_at(p, t, slab, r).token;
+      store_hidden(p, r, n, in, in ? hidden_value(p, t, slab, r, tok, n, s0, s1) : 0.0f);
+    }
+  }
+  return true;
+}
+
+__device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, int& local) {
+  const DecodeArgs& a = p.a;
+  Ctl& c = *t.c;
+  const int warp = threadIdx.x >> 5, lane = lane_id(), q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+  const int terms = a.terms == 2 ? 2 : 1, per = 8 / terms;
+  const int nl = half * 128 + q * 32 + lane;  // this thread's column of the tile
+  const int slabs = a.E + a.num_shared;
+  const int64_t tile_steps = static_cast<int64_t>(c.active) * f.nk;  // steps of one output tile, all groups
+  bool inner_ready = a.lora.n == 0 || a.lora.a[2] == nullptr;
+  auto* y = static_cast<__nv_bfloat16*>(a.y);
+  for (int64_t s = f.lo; s < f.hi;) {
+    const int64_t s0 = s / tile_steps * tile_steps, s1 = s0 + tile_steps;
+    const int j = static_cast<int>(s / tile_steps), n = j * 256 + nl;
+    const bool in = n < a.d;
+    for (int tk = 0; tk < a.S; ++tk) t.y[tk * 256 + nl] = 0.0f;
+    for (; s < f.hi && s < s1; ++local) {
+      const Unit u = unit_at(f, s);
+      s += u.k1 - u.k0;
+      const int g = u.tile % c.active, slab = c.slab[g], row0 = c.first[g], cnt = c.first[g + 1] - row0;
+      if (!inner_ready && u.k0 == 0) {
+        if (!epi_wait(p, kCoded, &c.abort)) return false;
+        inner_ready = true;
+      }
+      const int acc = local & 1;
+      bool failed = false;
+      if (!mbar_wait(&c.tfull[acc], (local >> 1) & 1, &c.abort)) {
+        if (lane == 0) give_up(p, &c.abort);
+        failed = true;
+      }
+      if (epi_any(failed)) return false;
+      tc_fence_after();
+      const uint32_t tb = c.tmem_base + acc * kAccCols + half * (kAccCols / 2) + (static_cast<uint32_t>(q * 32) << 16);
+      const int64_t och = static_cast<int64_t>(slab) * a.d + n;
+      const float cs = a.terms && in ? __ldg(a.s_out + och) : 1.0f;
+      const float bias = a.b_out != nullptr && in && u.k0 == 0 ? __ldg(a.b_out + och) : 0.0f;
+      for (int ch = 0; ch * per < cnt; ++ch) {
+        float v[8];
+        load_sums(tb + ch * 8, terms, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int tk = ch * per + i;
+          if (i >= per || tk >= cnt) break;
+          const int r = row0 + tk;
+          const Row row = row_at(p, t, slab, r);
+          float o = v[i];
+          if (a.terms) o *= __ldcg(p.hs + r) * cs;
+          if (u.k0 == 0) {
+            o += bias;
+            if (in && a.lora.n > 0 && a.lora.a[2] != nullptr && c.adapter[row.token] >= 0)
+              o += adapter_delta(a.lora, 2, slabs, c.adapter[row.token], slab, a.d, n,
+                                 p.u_out + static_cast<int64_t>(r) * a.lora.r);
+          }
+          t.y[row.token * 256 + nl] += row.gate * o;
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&c.tempty[acc]);
+    }
+    const Join jn = join_of(f, s0, s1);
+    if (jn.c0 == jn.c1) {
+      for (int tk = 0; tk < a.S; ++tk)
+        if (in) y[static_cast<int64_t>(tk) * a.d + n] = __float2bfloat16_rn(t.y[tk * 256 + nl]);
+      continue;
+    }
+    float* part = partial_of(p, jn, blockIdx.x);
+    for (int tk = 0; tk < a.S; ++tk) part[tk * 256 + nl] = t.y[tk * 256 + nl];
+    if (!join_last(p, t, jn, 1)) continue;
+    for (int tk = 0; tk < a.S; ++tk) {
+      const float v = join_sum(p, jn, tk * 256 + nl);
+      if (in) y[static_cast<int64_t>(tk) * a.d + n] = __float2bfloat16_rn(v);
+    }
+  }
+  return true;
+}
+
+__device__ void epilogue(const Params& p, const Tables& t, const Phase& up, const Phase& down) {
+  const DecodeArgs& a = p.a;
+  Ctl& c = *t.c;
+  int local = 0;
+  const bool inner_up = a.lora.n > 0 && (a.lora.a[0] != nullptr || a.lora.a[1] != nullptr);
+  const bool inner_down = a.lora.n > 0 && a.lora.a[2] != nullptr;
+  if (inner_up) {
+    adapter_inner(p, t, 0, 2);
+    epi_arrive(p, kInnerUp);
+  }
+  if (!epilogue_up(p, t, up, local)) return;
+  epi_arrive(p, kHidden);
+  if (a.terms || inner_down) {
+    if (!epi_wait(p, kHidden, &c.abort)) return;
+    if (a.terms) code_hidden(p, t);
+    if (inner_down) adapter_inner(p, t, 2, 1);
+    epi_arrive(p, kCoded);
+    if (a.terms && !epi_wait(p, kCoded, &c.abort)) return;  // the codes' row scales
+  }
+  epilogue_down(p, t, down, local);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap m_in0, const __grid_constant__ CUtensorMap m_in1,
+                  const __grid_constant__ CUtensorMap m_out, const __grid_constant__ CUtensorMap m_x,
+                  const __grid_constant__ CUtensorMap m_hidden, const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const DecodeArgs& a = p.a;
+  Tables t;
+  uint8_t* at = ring + p.ring_bytes;
+  t.c = reinterpret_cast<Ctl*>(at);
+  at += (sizeof(Ctl) + 15) & ~size_t(15);
+  t.y = reinterpret_cast<float*>(at);
+  at += static_cast<size_t>(a.S) * 256 * 4;
+  t.gate = reinterpret_cast<float*>(at);
+  at += static_cast<size_t>(a.S) * a.K * 4;
+  t.idx = reinterpret_cast<int*>(at);
+  at += static_cast<size_t>(a.S) * a.K * 4;
+  t.row_slot = reinterpret_cast<uint16_t*>(at);
+  Ctl& c = *t.c;
+  const int warp = threadIdx.x >> 5;
+  if (warp == 1) {
+    if (lane_id() == 0) {
+      for (int i = 0; i < p.stages; ++i) {
+        mbar_init(&c.full_w[i], 1);
+        mbar_init(&c.full_b[i], 1);
+        mbar_init(&c.empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&c.tfull[i], 1);
+        mbar_init(&c.tempty[i], kEpiThreads);
+      }
+      mbar_init(&c.drain, 1);
+      c.abort = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(&c.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   route_phase(p);
-  bool ok = grid_barrier(p, t, ++phase);
-  if (ok) {
+  if (grid_barrier(p, c, kRouted)) {
     tables_phase(p, t);
-    if (a.lora.n > 0) {
-      adapter_inner(p, t, 0, 2);
-      ok = grid_barrier(p, t, ++phase);
-    }
+    const bool pair = a.activation == MOE_ACT_SWIGLU;
+    const int bk = a.terms ? 128 : 64;
+    const int up_tiles = (a.h + (pair ? 127 : 255)) / (pair ? 128 : 256);
+    const Phase up = phase_of(c.active * up_tiles, (a.d + bk - 1) / bk);
+    const Phase down = phase_of(c.active * ((a.d + 255) / 256), (a.h + bk - 1) / bk);
+    if (warp == 0)
+      produce(p, t, ring, up, down, Maps{&m_in0, pair ? &m_in1 : &m_in0, &m_x, nullptr},
+              Maps{&m_out, &m_out, nullptr, &m_hidden});
+    else if (warp == 1 && lane_id() == 0)
+      multiply(p, t, ring, up, down);
+    else if (warp >= kEpiWarp0)
+      epilogue(p, t, up, down);
+    __syncwarp();
   }
-  if (ok) {
-    up_phase(p, t);
-    ok = grid_barrier(p, t, ++phase);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(c.tmem_base, kTmemCols);
   }
-  if (ok && (a.terms || a.lora.n > 0)) {
-    if (a.terms) {
-      const int rows = t.first[t.active];
-      for (int r = blockIdx.x + gridDim.x * (threadIdx.x >> 5); r < rows; r += gridDim.x * kWarps)
-        code_hidden_row(p.hidden + static_cast<int64_t>(r) * a.h, p.hq + static_cast<int64_t>(r) * a.terms * a.h,
-                        p.hs + r, a.h, a.terms);
-    }
-    if (a.lora.n > 0 && a.lora.a[2] != nullptr) adapter_inner(p, t, 2, 1);
-    ok = grid_barrier(p, t, ++phase);
-  }
-  if (ok) down_phase(p, t);
   leave(p);
 }
 
@@ -467,6 +1064,15 @@ size_t decode_workspace_bytes(int S, int d, int E, int K, int h, int num_shared,
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_set{0};  // one bit per device ordinal (host threads may launch concurrently)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(attr_set.load(std::memory_order_relaxed) & (1ull << dev))) {
+    e = cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemLimit));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   const Ws L = ws_layout(a.S, a.d, a.E, a.K, a.h, a.num_shared, a.terms, a.lora.n > 0 ? a.lora.r : 0);
   char* ws = static_cast<char*>(a.ws);
   Params p;
@@ -475,16 +1081,38 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   p.xq = reinterpret_cast<uint8_t*>(ws + L.xq);
   p.xs = reinterpret_cast<float*>(ws + L.xs);
   p.hidden = reinterpret_cast<__nv_bfloat16*>(ws + L.hidden);
+  p.amax = reinterpret_cast<uint32_t*>(ws + L.amax);
   p.hq = reinterpret_cast<uint8_t*>(ws + L.hq);
   p.hs = reinterpret_cast<float*>(ws + L.hs);
   p.u_in = reinterpret_cast<float*>(ws + L.u_in);
   p.u_out = reinterpret_cast<float*>(ws + L.u_out);
+  p.joins = reinterpret_cast<uint32_t*>(ws + L.joins);
+  p.partial = reinterpret_cast<float*>(ws + L.partial);
   p.status = reinterpret_cast<StatusBlock*>(ws);
   p.sync = reinterpret_cast<GridSync*>(ws + kSyncOffset);
+  const int terms = a.terms == 2 ? 2 : 1, eb = a.terms ? 1 : 2;
+  // a stage: two weight tiles, then the columns of the largest possible group
+  p.stage_bytes = 2 * kTileBytes + ((a.S * terms + 15) & ~15) * 128;
+  const size_t fixed = 1024 + tables_bytes(a.S, a.K, a.num_shared);
+  p.stages = static_cast<int>((kSmemLimit - fixed) / p.stage_bytes);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  if (p.stages < 2) return cudaErrorInvalidValue;
+  p.ring_bytes = p.stages * p.stage_bytes;
+  const int slabs = a.E + a.num_shared;
+  const int64_t rows = static_cast<int64_t>(a.S) * (a.K + a.num_shared);
+  CUtensorMap in0, in1, out, mx, mh;
+  if (!gemm::make_slab_map(&in0, a.w_in[0], slabs, a.h, a.d, eb) || !gemm::make_slab_map(&out, a.w_out, slabs, a.d, a.h, eb))
+    return cudaErrorInvalidValue;
+  in1 = in0;
+  if (a.w_in[1] != nullptr && !gemm::make_slab_map(&in1, a.w_in[1], slabs, a.h, a.d, eb)) return cudaErrorInvalidValue;
+  // tokens: rows gathered one by one; hidden rows: boxes of 16
+  if (!gemm::make_map(&mx, a.terms ? static_cast<const void*>(p.xq) : a.x, static_cast<int64_t>(a.S) * terms, a.d, 1, eb) ||
+      !gemm::make_map(&mh, a.terms ? static_cast<const void*>(p.hq) : p.hidden, rows * terms, a.h, 16, eb))
+    return cudaErrorInvalidValue;
   const int grid = a.num_sms < kDecodeMaxCtas ? a.num_sms : kDecodeMaxCtas;
-  void* args[] = {&p};
+  void* args[] = {&in0, &in1, &out, &mx, &mh, &p};
   return cudaLaunchCooperativeKernel(reinterpret_cast<void*>(decode_kernel), dim3(grid), dim3(kThreads), args,
-                                     sizeof(Tables), stream);
+                                     p.ring_bytes + fixed, stream);
 }
 
 }  // namespace moe

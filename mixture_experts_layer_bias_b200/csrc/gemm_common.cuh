@@ -225,6 +225,23 @@ inline bool make_store_map(CUtensorMap* m, void* base, int64_t rows, int cols, i
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D map over [slabs][rows][k] weights; box = one 128-byte swizzle row of k
+// by 128 rows of one slab (rows past the slab's end are filled with zeros).
+inline bool make_slab_map(CUtensorMap* m, const void* base, int64_t slabs, int rows, int k, int elem_bytes) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (enc == nullptr || slabs <= 0 || rows <= 0 || k <= 0) return false;
+  const cuuint64_t row_bytes = static_cast<cuuint64_t>(k) * elem_bytes;
+  if ((reinterpret_cast<uintptr_t>(base) & 15) != 0 || row_bytes % 16 != 0) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(slabs)};
+  cuuint64_t strides[2] = {row_bytes, row_bytes * rows};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem_bytes), 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 inline bool make_map(CUtensorMap* m, const void* base, int64_t rows, int k, int box_rows = 128, int elem_bytes = 2) {
   EncodeTiledFn enc = get_encode_fn();
   if (enc == nullptr || rows <= 0 || k <= 0) return false;
