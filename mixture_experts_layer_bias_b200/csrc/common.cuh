@@ -186,17 +186,6 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
-// Four rows r0 .. r3 of a 2-D map whose box is one row high, to four
-// consecutive shared-memory rows.
-__device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* m, int c0, int r0, int r1, int r2,
-                                            int r3, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-      : "memory");
-}
-
 // Order this thread's generic-proxy global-memory accesses and async-proxy
 // (TMA) ones, in both directions.
 __device__ __forceinline__ void fence_proxy_async_global() {

@@ -6,11 +6,15 @@
 // With a handful of tokens the layer is bound by reading the touched experts'
 // weights once, and a chain of kernels leaves HBM idle at every boundary.
 // Here the steps are phases of one grid:
-//   route    logits, a warp per (expert, 8 tokens); with E4M3 weights also the
-//            tokens' row codes; grid barrier; then every CTA selects all
-//            tokens by itself and builds the expert groups in shared memory
+//   route    logits in fp64, a CTA per (expert, 8 tokens); with E4M3 weights
+//            also the tokens' row codes; then the selection and the expert
+//            groups, which every CTA builds in its own shared memory
 //   up       hidden = act(x W_in)
 //   down     y = sum_k g_k hidden_k W_out
+//
+// Logits and selection keys are fp64 (bf16 products are exact in fp32, their
+// sum is not), so the choice between two experts is that of the exact keys
+// however close they are.
 //
 // The two products run on the 5th-generation tensor cores with the WEIGHTS as
 // the M = 128 operand and a group's tokens as the N = 16 .. 128 columns, so no
@@ -20,13 +24,20 @@
 // one token tile: gate and up rows of the same 128 hidden columns (SwiGLU), or
 // 256 neighbouring output columns.  All steps of a phase, in the order (group,
 // tile, k) for up and (tile, group, k) for down, are cut into one equal range
-// per CTA, so every SM reads the same bytes whatever the group sizes are; a
+// per CTA, so every SM reads the same bytes whatever the group sizes are.  An up
 // tile cut by a range border is joined through fp32 partial sums in the
-// workspace by whichever CTA arrives last, always in CTA order.
+// workspace by whichever CTA arrives last; the down phase's sums all go through
+// such partial tiles and are added by the whole grid at the end.  Both add in
+// CTA order, so results do not depend on timing.
 //
-// Roles (384 threads): warp 0 feeds a ring of stages by TMA (the tokens by
-// 4-row gathers straight from x), warp 1 issues the MMAs, warps 4 - 11 are the
-// epilogue, two per TMEM lane quarter.  The weights of the down phase do not
+// Token tile of the up phase: while all tokens fit into the 16 columns that an
+// MMA has at least, every group uses all of them, straight from x.  Otherwise
+// the token rows (or codes) are first copied group by group and a group's
+// columns are its own tokens.  (Gathering the rows by TMA, four at a time,
+// held the up phase at 4.8 TB/s for one token.)
+//
+// Roles (384 threads): warp 0 feeds a ring of stages by TMA, warp 1 issues the
+// MMAs, warps 4 - 11 are the epilogue, two per TMEM lane quarter.  The weights of the down phase do not
 // depend on the hidden rows, so the producer fills the whole ring with them
 // while the up phase drains and the grid waits for the last hidden row.
 //
@@ -50,16 +61,11 @@
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
-#include "route_select.cuh"
 #include "row_coding.cuh"
 
 namespace moe {
 
 namespace {
-
-using route_detail::select_topk;
-using route_detail::SelectParams;
-using route_detail::warp_sum;
 
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
@@ -76,7 +82,7 @@ constexpr size_t kSmemLimit = 232448;  // 227 KB per CTA
 // Grid-wide arrival counters, in the workspace's first 256 bytes behind the
 // status block: they count up within one call; the last CTA to leave the
 // kernel sets them back to zero.
-enum Arrival { kRouted = 0, kInnerUp = 1, kHidden = 2, kCoded = 3, kNumArrivals = 4 };
+enum Arrival { kRouted, kSelected, kPacked, kInnerUp, kHidden, kCoded, kSummed, kNumArrivals };
 struct GridSync {
   uint32_t arrived[kNumArrivals];
   uint32_t left;
@@ -86,10 +92,13 @@ static_assert(sizeof(StatusBlock) <= kSyncOffset, "the arrival counters sit behi
 static_assert(kSyncOffset + sizeof(GridSync) <= 256, "the arrival counters sit in the initialised block");
 
 struct Ws {
-  size_t logits, xq, xs, hidden, amax, hq, hs, u_in, u_out, joins, partial, total;
+  size_t logits, idx, gate, xq, xs, xp, hidden, amax, hq, hs, u_in, u_out, joins, partial, total;
 };
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+// Whether the up phase's token tile holds all tokens (see above).
+__host__ __device__ constexpr bool all_tokens(int S, int terms) { return S * (terms == 2 ? 2 : 1) <= 16; }
 
 Ws ws_layout(int S, int d, int E, int K, int h, int ns, int terms, int rank) {
   Ws L;
@@ -100,17 +109,20 @@ Ws ws_layout(int S, int d, int E, int K, int h, int ns, int terms, int rank) {
     return at;
   };
   const size_t rows = static_cast<size_t>(S) * (K + ns);
-  L.logits = take(static_cast<size_t>(S) * E * 4);
+  L.logits = take(static_cast<size_t>(S) * E * 8);
+  L.idx = take(static_cast<size_t>(S) * K * 4);
+  L.gate = take(static_cast<size_t>(S) * K * 4);
   L.xq = take(static_cast<size_t>(terms) * S * d);
   L.xs = take(terms ? static_cast<size_t>(S) * 4 : 0);
+  L.xp = take(all_tokens(S, terms) ? 0 : rows * d * (terms ? terms : 2));
   L.hidden = take(rows * h * 2);
   L.amax = take(terms ? rows * 4 : 0);
   L.hq = take(static_cast<size_t>(terms) * rows * h);
   L.hs = take(terms ? rows * 4 : 0);
   L.u_in = take(rows * 2 * rank * 4);
   L.u_out = take(rows * rank * 4);
-  // per CTA: a counter of its first cut tile for each phase, and two tiles' partial sums
-  L.joins = take(2 * kDecodeMaxCtas * 4);
+  // per CTA: a counter for the cut up tile that begins in it, and two tiles' partial sums
+  L.joins = take(kDecodeMaxCtas * 4);
   L.partial = take(static_cast<size_t>(kDecodeMaxCtas) * 2 * S * 256 * 4);
   L.total = o;
   return L;
@@ -118,9 +130,12 @@ Ws ws_layout(int S, int d, int E, int K, int h, int ns, int terms, int rank) {
 
 struct Params {
   DecodeArgs a;
-  float* logits;
+  double* logits;
+  int* idx;     // the selection, where it is made by several CTAs
+  float* gate;
   uint8_t* xq;
   float* xs;
+  uint8_t* xp;  // token rows or codes, group by group
   __nv_bfloat16* hidden;
   uint32_t* amax;
   uint8_t* hq;
@@ -148,12 +163,23 @@ struct Ctl {
   int last;
   int warp_sums[kWarps];
   int first[kMaxSlabs + 1];            // active group -> its first row
+  int row0[kMaxSlabs];                 // slab -> its first row
   int slab[kMaxSlabs];                 // active group -> weight slab
+  uint64_t mask[kMaxSlabs];            // active group -> its tokens
+  uint64_t tokens_of[kMaxSlabs];       // slab -> its tokens
   int adapter[MOE_DECODE_MAX_TOKENS];  // token -> adapter or -1
+};
+
+// Scratch of the routing, in the ring before its first copy.
+struct Scratch {
+  uint64_t key[kThreads];   // ordered keys
+  double score[kThreads];   // gate sources
+  double sum[kThreads];     // logits: warp sums; selection: group scores, then the picks' gate sources
 };
 
 struct Tables {
   Ctl* c;
+  Scratch* scratch;
   float* gate;         // [S][K]
   int* idx;            // [S][K]
   uint16_t* row_slot;  // row -> slot t*K + k (shared rows: token)
@@ -254,18 +280,10 @@ __device__ void leave(const Params& p) {
   }
 }
 
-// Sum over a warp of the products of two bf16 rows; `row` may have been
-// written by this grid, so it is read at L2.
-__device__ float warp_dot(const __nv_bfloat16* w, const __nv_bfloat16* row, int n) {
-  float acc = 0.0f;
-  for (int c = lane_id() * 8; c < n; c += 256) {
-    float a[8], b[8];
-    coding::bf16x8_to_f32(ldg16(w + c), a);
-    coding::bf16x8_to_f32(__ldcg(reinterpret_cast<const uint4*>(row + c)), b);
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc = fmaf(a[j], b[j], acc);
-  }
-  return warp_sum(acc);
+  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+  return v;
 }
 
 // scale * sum_r u[r] B[a][slab][n][r], by one thread.
@@ -290,82 +308,207 @@ __device__ float adapter_delta(const LoraParams& l, int m, int slabs, int a, int
   return acc * __ldg(l.scale + a);
 }
 
-template <int NI>
-__device__ void select_tokens(const Params& p, const SelectParams& sp) {
-  const int warp = threadIdx.x >> 5, lane = lane_id();
-  for (int tok = warp; tok < p.a.S; tok += kWarps) {
-    float l[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int e = 32 * i + lane;
-      l[i] = e < p.a.E ? __ldcg(p.logits + static_cast<int64_t>(tok) * p.a.E + e) : 0.0f;
-    }
-    select_topk<NI>(l, sp, tok);
-  }
-}
-
-// Router logits and, with E4M3 weights, the tokens' codes; the join counters
-// and row maxima of this call start at zero.
-__device__ void route_phase(const Params& p) {
+// Router logits, a CTA per (expert, 8 tokens), the threads striding over d in
+// 16-byte pieces: a bf16 product is exact in fp32 and is summed in fp64.  With
+// E4M3 weights also the tokens' codes, a warp per token, by the CTAs from the
+// other end of the grid.  The join counters and row maxima start at zero.
+__device__ void route_phase(const Params& p, Scratch& c) {
   const DecodeArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = lane_id();
   const int rows = a.S * (a.K + a.num_shared);
-  for (int i = blockIdx.x * kThreads + threadIdx.x; i < 2 * kDecodeMaxCtas || (a.terms && i < rows);
-       i += gridDim.x * kThreads) {
-    if (i < 2 * kDecodeMaxCtas) p.joins[i] = 0;
+  for (int i = blockIdx.x * kThreads + tid; i < kDecodeMaxCtas || (a.terms && i < rows); i += gridDim.x * kThreads) {
+    if (i < kDecodeMaxCtas) p.joins[i] = 0;
     if (a.terms && i < rows) p.amax[i] = 0;
   }
-  const int warp = threadIdx.x >> 5, lane = lane_id();
-  const int tb = (a.S + kRouteTokens - 1) / kRouteTokens;
-  const int dots = a.E * tb, items = dots + (a.terms ? a.S : 0);
   const auto* x = static_cast<const __nv_bfloat16*>(a.x);
-  for (int i = blockIdx.x + gridDim.x * warp; i < items; i += gridDim.x * kWarps) {
-    if (i >= dots) {
-      const int t = i - dots;
+  if (a.terms) {
+    for (int t = (gridDim.x - 1 - blockIdx.x) + gridDim.x * warp; t < a.S; t += gridDim.x * kWarps)
       coding::code_row<32>(x + static_cast<int64_t>(t) * a.d, p.xq + static_cast<int64_t>(t) * a.terms * a.d,
                            p.xs + t, a.d, a.terms, lane);
-      continue;
-    }
-    const int e = i % a.E, t0 = (i / a.E) * kRouteTokens;
+  }
+  const int items = a.E * ((a.S + kRouteTokens - 1) / kRouteTokens);
+  for (int i = blockIdx.x; i < items; i += gridDim.x) {
+    const int e = i % a.E, t0 = (i / a.E) * kRouteTokens, nt = min(kRouteTokens, a.S - t0);
     const auto* w = static_cast<const __nv_bfloat16*>(a.w_router) + static_cast<int64_t>(e) * a.d;
-    float acc[kRouteTokens];
+    const auto* xt = x + static_cast<int64_t>(t0) * a.d;
+    double acc[kRouteTokens];
 #pragma unroll
-    for (int j = 0; j < kRouteTokens; ++j) acc[j] = 0.0f;
-    for (int c = lane * 8; c < a.d; c += 256) {
+    for (int j = 0; j < kRouteTokens; ++j) acc[j] = 0.0;
+    for (int k = tid * 8; k < a.d; k += kThreads * 8) {
       float wf[8];
-      coding::bf16x8_to_f32(ldg16(w + c), wf);
+      uint4 xv[kRouteTokens];
+      const uint4 wv = ldg16(w + k);
+#pragma unroll
+      for (int j = 0; j < kRouteTokens; ++j)
+        if (j < nt) xv[j] = ldg16(xt + static_cast<int64_t>(j) * a.d + k);
+      coding::bf16x8_to_f32(wv, wf);
 #pragma unroll
       for (int j = 0; j < kRouteTokens; ++j) {
-        if (t0 + j < a.S) {
+        if (j < nt) {
           float xf[8];
-          coding::bf16x8_to_f32(ldg16(x + static_cast<int64_t>(t0 + j) * a.d + c), xf);
+          coding::bf16x8_to_f32(xv[j], xf);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) acc[j] = fmaf(wf[q], xf[q], acc[j]);
+          for (int q = 0; q < 8; ++q) acc[j] += static_cast<double>(__fmul_rn(wf[q], xf[q]));
         }
       }
     }
-    const float bias = a.router_bias != nullptr ? __ldg(a.router_bias + e) : 0.0f;
 #pragma unroll
     for (int j = 0; j < kRouteTokens; ++j) {
-      const float s = warp_sum(acc[j]);
-      if (lane == 0 && t0 + j < a.S) p.logits[static_cast<int64_t>(t0 + j) * a.E + e] = __fadd_rn(s, bias);
+      if (j < nt) {
+        double v = acc[j];
+        for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+        if (lane == 0) c.sum[warp * kRouteTokens + j] = v;
+      }
     }
+    __syncthreads();
+    if (tid < nt) {
+      double v = a.router_bias != nullptr ? static_cast<double>(__ldg(a.router_bias + e)) : 0.0;
+      for (int k = 0; k < kWarps; ++k) v += c.sum[k * kRouteTokens + tid];
+      p.logits[static_cast<int64_t>(t0 + tid) * a.E + e] = v;
+    }
+    __syncthreads();
   }
 }
 
-// Selection of every token and the group tables, by each CTA for itself.
-__device__ void tables_phase(const Params& p, const Tables& t) {
+// A double as an unsigned integer of the same order; all results are above 0.
+__device__ __forceinline__ uint64_t ordered(double v) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v));
+  return (b >> 63) ? ~b : b | (uint64_t(1) << 63);
+}
+
+// Tokens that a CTA selects at once: a thread per (token, expert).
+__device__ __forceinline__ int select_width(int E) {
+  int w = 32;
+  while (w < E) w <<= 1;
+  return w;
+}
+
+// Selection of the tokens t0 .. t0 + n - 1 (n * width <= kThreads) by the whole
+// CTA: an expert's slot is the number of candidates with a larger key (ties to
+// the lower index; a NaN key ranks as -inf).  Scores, group limit and gates as
+// in the routing kernels, with fp64 keys.
+__device__ void select_tokens(const Params& p, Scratch& c, int t0, int n, int width, int* idx, float* gate, bool report_bad) {
   const DecodeArgs& a = p.a;
+  const int tid = threadIdx.x, j = tid / width, e = tid % width;
+  const double kNegInf = __longlong_as_double(0xfff0000000000000ll);
+  const bool in = j < n && e < a.E;
+  double score = 0.0, key = kNegInf;
+  if (in) {
+    const double l = __ldcg(p.logits + static_cast<int64_t>(t0 + j) * a.E + e);
+    score = a.score_fn == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-l)) : l / static_cast<double>(a.tau);
+    key = a.sel_bias != nullptr ? score + static_cast<double>(__ldg(a.sel_bias + e)) : score;
+    if (isnan(key)) key = kNegInf;
+    c.score[tid] = score;
+    c.key[tid] = ordered(key);
+    if (report_bad) {
+      // one report per token: by its first bad expert
+      if (!isfinite(l)) {
+        bool first = true;
+        for (int q = 0; q < e && first; ++q)
+          first = isfinite(__ldcg(p.logits + static_cast<int64_t>(t0 + j) * a.E + q));
+        if (first) report(p.status, MOE_STATUS_NONFINITE_LOGIT, MOE_CNT_NONFINITE);
+      }
+    }
+  }
+  __syncthreads();
+  if (a.num_groups > 1) {
+    const int gs = a.E / a.num_groups;
+    double s = 0.0;
+    if (j < n && e < a.num_groups) {
+      for (int q = 0; q < gs; ++q) {
+        const uint64_t o = c.key[j * width + e * gs + q];
+        s += __longlong_as_double(static_cast<long long>((o >> 63) ? o ^ (uint64_t(1) << 63) : ~o));
+      }
+      if (isnan(s)) s = kNegInf;
+      c.sum[tid] = s;
+    }
+    __syncthreads();
+    bool kept = false;
+    if (in) {
+      const int g = e / gs;
+      const double mine = c.sum[j * width + g];
+      int rank = 0;
+      for (int q = 0; q < a.num_groups; ++q) {
+        const double o = c.sum[j * width + q];
+        rank += o > mine || (o == mine && q < g);
+      }
+      kept = rank < a.topk_groups;
+    }
+    __syncthreads();
+    if (in && !kept) c.key[tid] = 0;  // below every candidate
+    __syncthreads();
+  }
+  int rank = a.K;
+  if (in) {
+    const uint64_t mine = c.key[tid];
+    rank = 0;
+    for (int q = 0; q < a.E; ++q) {
+      const uint64_t o = c.key[j * width + q];
+      rank += o > mine || (o == mine && q < e);
+    }
+    if (rank < a.K) {
+      idx[(t0 + j) * a.K + rank] = e;
+      c.sum[j * width + rank] = score;  // (the group scores have been read)
+    }
+  }
+  __syncthreads();
+  if (j < n && e < a.K) {
+    const double* picks = c.sum + j * width;
+    const double mine = picks[e];
+    float g;
+    if (a.score_fn == MOE_SCORE_SOFTMAX) {
+      const double* from = a.renormalize ? picks : c.score + j * width;
+      const int m = a.renormalize ? a.K : a.E;
+      double top = kNegInf;
+      bool nan = false;
+      for (int q = 0; q < m; ++q) {
+        top = fmax(top, from[q]);
+        nan |= isnan(from[q]);
+      }
+      float sum = 0.0f;
+      for (int q = 0; q < m; ++q) sum += expf(static_cast<float>(from[q] - top));
+      g = expf(static_cast<float>(mine - top)) / sum;
+      if (nan) g = __int_as_float(0x7fc00000);
+    } else if (a.renormalize) {
+      double sum = 0.0;
+      for (int q = 0; q < a.K; ++q) sum += picks[q];
+      g = static_cast<float>(mine / sum);
+    } else {
+      g = static_cast<float>(mine);
+    }
+    gate[(t0 + j) * a.K + e] = g;
+  }
+  __syncthreads();
+}
+
+// Selection and the group tables in this CTA's shared memory.  Up to two rounds
+// of tokens are selected by every CTA for itself; more are spread over the CTAs
+// (a grid barrier costs less than a third round).  False: a wait gave up.
+__device__ bool tables_phase(const Params& p, const Tables& t) {
+  const DecodeArgs& a = p.a;
+  Ctl& c = *t.c;
   const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
-  SelectParams sp{a.E,        a.K,    a.score_fn, a.renormalize, a.num_groups, a.topk_groups, a.tau,
-                  a.sel_bias, t.idx,  t.gate,     blockIdx.x == 0 ? p.status : nullptr, nullptr, nullptr};
-  if (a.E <= 32)
-    select_tokens<1>(p, sp);
-  else if (a.E <= 64)
-    select_tokens<2>(p, sp);
-  else if (a.E <= 128)
-    select_tokens<4>(p, sp);
-  else
-    select_tokens<8>(p, sp);
+  const int slots = a.S * a.K, slabs = a.E + a.num_shared;
+  const int width = select_width(a.E), per = kThreads / width, rounds = (a.S + per - 1) / per;
+  for (int i = tid; i < slabs; i += kThreads) c.tokens_of[i] = 0;
+  if (rounds <= 2) {
+    for (int r = 0; r < rounds; ++r)
+      select_tokens(p, *t.scratch, r * per, min(per, a.S - r * per), width, t.idx, t.gate, blockIdx.x == 0);
+  } else {
+    for (int r = blockIdx.x; r < rounds; r += gridDim.x)
+      select_tokens(p, *t.scratch, r * per, min(per, a.S - r * per), width, p.idx, p.gate, true);
+    if (!grid_barrier(p, c, kSelected)) return false;
+    for (int i = tid; i < slots; i += kThreads) {
+      t.idx[i] = __ldcg(p.idx + i);
+      t.gate[i] = __ldcg(p.gate + i);
+    }
+    __syncthreads();
+  }
+  fence_proxy_async_smem();  // the scratch lies where the first copies land
+  // an expert's tokens as a 64-bit mask: its rows are the set bits in token order
+  for (int i = tid; i < slots; i += kThreads)
+    atomicOr(reinterpret_cast<unsigned long long*>(c.tokens_of + t.idx[i]), 1ull << (i / a.K));
+  if (tid == 0 && a.num_shared) c.tokens_of[a.E] = a.S == 64 ? ~uint64_t(0) : (uint64_t(1) << a.S) - 1;
   if (a.lora.n > 0) {
     for (int i = tid; i < a.S; i += kThreads) {
       int id = __ldg(a.lora.ids + i);
@@ -373,19 +516,13 @@ __device__ void tables_phase(const Params& p, const Tables& t) {
         if (blockIdx.x == 0) report(p.status, MOE_STATUS_BAD_ADAPTER, -1);
         id = -1;
       }
-      t.c->adapter[i] = id;
+      c.adapter[i] = id;
     }
   }
   __syncthreads();
-  // thread e: the rows of expert e, in slot order
-  const int slots = a.S * a.K, slabs = a.E + a.num_shared;
-  int count = 0;
-  if (tid < a.E) {
-    for (int i = 0; i < slots; ++i) count += t.idx[i] == tid;
-  } else if (tid < slabs) {
-    count = a.S;
-  }
   // exclusive prefix over the slabs of (rows, active groups)
+  const uint64_t mask = tid < slabs ? c.tokens_of[tid] : 0;
+  const int count = __popcll(mask);
   const int v = count | (count > 0 ? 1 << 16 : 0);
   int incl = v;
 #pragma unroll
@@ -393,27 +530,29 @@ __device__ void tables_phase(const Params& p, const Tables& t) {
     const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
     if (lane >= off) incl += o;
   }
-  if (lane == 31) t.c->warp_sums[warp] = incl;
+  if (lane == 31) c.warp_sums[warp] = incl;
   __syncthreads();
   int before = incl - v;
-  for (int w = 0; w < warp; ++w) before += t.c->warp_sums[w];
+  for (int w = 0; w < warp; ++w) before += c.warp_sums[w];
   const int row0 = before & 0xFFFF, group = before >> 16;
-  if (tid < slabs && count > 0) {
-    t.c->first[group] = row0;
-    t.c->slab[group] = tid;
-    if (tid < a.E) {
-      int r = row0;
-      for (int i = 0; i < slots; ++i)
-        if (t.idx[i] == tid) t.row_slot[r++] = static_cast<uint16_t>(i);
-    } else {
-      for (int i = 0; i < a.S; ++i) t.row_slot[row0 + i] = static_cast<uint16_t>(i);
-    }
+  if (count > 0) {
+    c.first[group] = row0;
+    c.slab[group] = tid;
+    c.mask[group] = mask;
   }
+  if (tid < slabs) c.row0[tid] = row0;
   if (tid == kThreads - 1) {
     const int all = before + v;
-    t.c->active = all >> 16;
-    t.c->first[all >> 16] = all & 0xFFFF;
+    c.active = all >> 16;
+    c.first[all >> 16] = all & 0xFFFF;
   }
+  __syncthreads();
+  for (int i = tid; i < slots; i += kThreads) {
+    const int e = t.idx[i], tok = i / a.K;
+    t.row_slot[c.row0[e] + __popcll(c.tokens_of[e] & ((uint64_t(1) << tok) - 1))] = static_cast<uint16_t>(i);
+  }
+  if (a.num_shared)
+    for (int i = tid; i < a.S; i += kThreads) t.row_slot[slots + i] = static_cast<uint16_t>(i);
   if (blockIdx.x == 0) {
     if (a.counts != nullptr && tid < a.E) a.counts[tid] = count;
     for (int i = tid; i < slots; i += kThreads) {
@@ -422,6 +561,25 @@ __device__ void tables_phase(const Params& p, const Tables& t) {
     }
   }
   __syncthreads();
+  if (all_tokens(a.S, a.terms)) return true;
+  // token rows or codes, group by group: a warp per row
+  const int rows = slots + a.S * a.num_shared, bytes = a.d * (a.terms ? a.terms : 2);
+  for (int r = blockIdx.x + gridDim.x * warp; r < rows; r += gridDim.x * kWarps) {
+    const int tok = r < slots ? t.row_slot[r] / a.K : t.row_slot[r];
+    const auto* src = reinterpret_cast<const uint4*>(
+        (a.terms ? p.xq : static_cast<const uint8_t*>(a.x)) + static_cast<int64_t>(tok) * bytes);
+    auto* dst = reinterpret_cast<uint4*>(p.xp + static_cast<int64_t>(r) * bytes);
+    for (int i = lane; i < bytes / 16; i += 128) {
+      uint4 q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + 32 * k < bytes / 16) q[k] = __ldcg(src + i + 32 * k);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + 32 * k < bytes / 16) dst[i + 32 * k] = q[k];
+    }
+  }
+  return grid_barrier(p, c, kPacked);
 }
 
 struct Row {
@@ -448,15 +606,17 @@ __device__ __forceinline__ int group_of_row(const Ctl& c, int r) {
   return lo;
 }
 
-// Epilogue warps: u[row][m][i] = A_m[a][slab][i] . row for the pairs m0 .. m0 + nm - 1.
+// Epilogue warps: u[row][m][i] = A_m[a][slab][i] . row for the pairs m0 .. m0 +
+// nm - 1, a warp per (row, pair, 8 values): the row's pieces meet eight rows of
+// A, nine loads in flight per lane and step.
 __device__ void adapter_inner(const Params& p, const Tables& t, int m0, int nm) {
   const LoraParams& l = p.a.lora;
-  const int rows = t.c->first[t.c->active], slabs = p.a.E + p.a.num_shared;
-  const int warp = (threadIdx.x >> 5) - kEpiWarp0;
+  const int rows = t.c->first[t.c->active], slabs = p.a.E + p.a.num_shared, blocks = l.r / 8;
+  const int warp = (threadIdx.x >> 5) - kEpiWarp0, lane = lane_id();
   const int n = m0 == 2 ? p.a.h : p.a.d;
   float* out = m0 == 2 ? p.u_out : p.u_in;
-  for (int i = blockIdx.x + gridDim.x * warp; i < rows * nm * l.r; i += gridDim.x * (kEpiThreads / 32)) {
-    const int j = i % l.r, m = m0 + (i / l.r) % nm, r = i / (l.r * nm);
+  for (int i = blockIdx.x + gridDim.x * warp; i < rows * nm * blocks; i += gridDim.x * (kEpiThreads / 32)) {
+    const int j = i % blocks * 8, m = m0 + (i / blocks) % nm, r = i / (blocks * nm);
     if (l.a[m] == nullptr) continue;
     const int slab = t.c->slab[group_of_row(*t.c, r)];
     const int token = row_at(p, t, slab, r).token, ad = t.c->adapter[token];
@@ -464,8 +624,31 @@ __device__ void adapter_inner(const Params& p, const Tables& t, int m0, int nm) 
     const auto* w = static_cast<const __nv_bfloat16*>(l.a[m]) + ((static_cast<int64_t>(ad) * slabs + slab) * l.r + j) * n;
     const __nv_bfloat16* src = m0 == 2 ? p.hidden + static_cast<int64_t>(r) * n
                                        : static_cast<const __nv_bfloat16*>(p.a.x) + static_cast<int64_t>(token) * n;
-    const float v = warp_dot(w, src, n);
-    if (lane_id() == 0) out[(static_cast<int64_t>(r) * nm + (m - m0)) * l.r + j] = v;
+    float acc[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+#pragma unroll 2
+    for (int c = lane * 8; c < n; c += 256) {
+      uint4 wv[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) wv[k] = ldg16(w + static_cast<int64_t>(k) * n + c);
+      float xf[8];
+      coding::bf16x8_to_f32(__ldcg(reinterpret_cast<const uint4*>(src + c)), xf);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float wf[8];
+        coding::bf16x8_to_f32(wv[k], wf);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[k] = fmaf(wf[q], xf[q], acc[k]);
+      }
+    }
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float s = warp_sum(acc[k]);
+      if (lane == k) v = s;
+    }
+    if (lane < 8) out[(static_cast<int64_t>(r) * nm + (m - m0)) * l.r + j + lane] = v;
   }
 }
 
@@ -485,80 +668,70 @@ __device__ void code_hidden(const Params& p, const Tables& t) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       v[k] = c0 + 256 * k < a.h ? __ldcg(reinterpret_cast<const uint4*>(src + c0 + 256 * k)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < 4; ++k)
       if (c0 + 256 * k < a.h) coding::code_piece(v[k], dst, a.h, c0 + 256 * k, a.terms, s, m);
     if (i % pieces == 0 && lane_id() == 0) p.hs[r] = s;
   }
 }
 
-// The steps of one phase and this CTA's range of them.  Unit: the part of one
-// tile that lies in the range.
+// The steps of one phase (32 bits: checked on the host), cut into `parts` ranges
+// of q or q + 1 steps, the longer ones first; this CTA's is [lo, hi).
 struct Phase {
-  int nk;         // steps of a tile (its K)
-  int64_t lo, hi; // this CTA's steps
-  int64_t total;
-  int parts;      // CTAs that have steps: every one of them at least one
+  int nk;     // steps of a tile (its K)
+  int total;
+  int parts;  // CTAs that have steps: every one of them at least one
+  int q, r;
+  int lo, hi;
+
+  __device__ __forceinline__ int begin_of(int c) const { return c * q + min(c, r); }
+  // the CTA whose range holds step s
+  __device__ __forceinline__ int part_of(int s) const {
+    const int longer = r * (q + 1);
+    return s < longer ? s / (q + 1) : r + (s - longer) / q;
+  }
 };
 
 __device__ __forceinline__ Phase phase_of(int tiles, int nk) {
   Phase f;
   f.nk = nk;
-  f.total = static_cast<int64_t>(tiles) * nk;
-  f.parts = f.total < gridDim.x ? static_cast<int>(f.total) : static_cast<int>(gridDim.x);
-  const int c = static_cast<int>(blockIdx.x);
-  f.lo = c < f.parts ? f.total * c / f.parts : f.total;
-  f.hi = c < f.parts ? f.total * (c + 1) / f.parts : f.total;
+  f.total = tiles * nk;
+  f.parts = min(f.total, static_cast<int>(gridDim.x));
+  f.q = f.total / f.parts;
+  f.r = f.total - f.q * f.parts;
+  const int c = min(static_cast<int>(blockIdx.x), f.parts);
+  f.lo = f.begin_of(c);
+  f.hi = c < f.parts ? f.begin_of(c + 1) : f.lo;
   return f;
 }
 
+// The part of one tile that lies in a range.
 struct Unit {
   int tile, k0, k1;
 };
 
-__device__ __forceinline__ Unit unit_at(const Phase& f, int64_t s) {
+__device__ __forceinline__ Unit unit_at(const Phase& f, int s) {
   Unit u;
-  u.tile = static_cast<int>(s / f.nk);
-  u.k0 = static_cast<int>(s - static_cast<int64_t>(u.tile) * f.nk);
-  const int64_t left = f.hi - s;
-  u.k1 = left < f.nk - u.k0 ? u.k0 + static_cast<int>(left) : f.nk;
+  u.tile = s / f.nk;
+  u.k0 = s - u.tile * f.nk;
+  u.k1 = min(f.nk, u.k0 + f.hi - s);
   return u;
 }
 
-// A tile that several CTAs share: the CTAs c0 .. c1 hold its steps from s0 on,
-// each with a partial tile of its own, element [tok][half * 128 + n].
-struct Join {
-  int c0, c1;
-  int64_t s0, total;
-  int parts;
-};
-
-__device__ __forceinline__ Join join_of(const Phase& f, int64_t s0, int64_t s1) {
-  // the CTA of step s: the largest c with floor(total c / parts) <= s, i.e. c < (s + 1) parts / total
-  return Join{static_cast<int>(((s0 + 1) * f.parts - 1) / f.total), static_cast<int>((s1 * f.parts - 1) / f.total), s0,
-              f.total, f.parts};
+// Partial tile of CTA c with part of the steps from s0 on, element [tok][half *
+// 128 + n]: 0 where the steps from s0 on began before its range, else 1.
+__device__ __forceinline__ float* partial_of(const Params& p, const Phase& f, int c, int s0) {
+  return p.partial + (static_cast<int64_t>(c) * 2 + (f.begin_of(c) > s0 ? 0 : 1)) * p.a.S * 256;
 }
 
-// Partial tile of CTA c: 0 for a tile that began before its range, else 1.
-__device__ __forceinline__ float* partial_of(const Params& p, const Join& j, int c) {
-  const int64_t lo = j.total * c / j.parts;
-  return p.partial + (static_cast<int64_t>(c) * 2 + (lo > j.s0 ? 0 : 1)) * p.a.S * 256;
-}
-
-__device__ __forceinline__ float join_sum(const Params& p, const Join& j, int at) {
-  float v = 0.0f;
-  for (int c = j.c0; c <= j.c1; ++c) v += __ldcg(partial_of(p, j, c) + at);
-  return v;
-}
-
-// The epilogue warps have written this CTA's part: true for all of them when
-// it was the last one.
-__device__ __forceinline__ bool join_last(const Params& p, const Tables& t, const Join& j, int phase) {
+// The epilogue warps have written this CTA's part of an up tile that the CTAs
+// c0 .. c1 share: true for all of them when it was the last one.
+__device__ __forceinline__ bool join_last(const Params& p, const Tables& t, int c0, int c1) {
   __threadfence();
   epi_any(false);
   if (threadIdx.x == 32 * kEpiWarp0) {
     __threadfence();
-    t.c->last = atomicAdd(p.joins + phase * kDecodeMaxCtas + j.c0, 1) == static_cast<uint32_t>(j.c1 - j.c0);
+    t.c->last = atomicAdd(p.joins + c0, 1) == static_cast<uint32_t>(c1 - c0);
   }
   epi_any(false);
   const bool last = t.c->last != 0;
@@ -576,11 +749,6 @@ struct Slot {
       round ^= 1;
     }
   }
-};
-
-// Output rows of one group's tile: which weight rows, which token rows.
-struct Maps {
-  const CUtensorMap *w0, *w1, *x, *hidden;
 };
 
 // Warp 0.  Weight tiles and token tiles have barriers of their own, so a stage's
@@ -614,42 +782,15 @@ struct Producer {
     return true;
   }
 
-  // Token tile of the up phase: the group's tokens, `terms` columns each.
-  __device__ void tokens(const CUtensorMap* m, int k, int row0, int n) {
+  // Token tile: `boxes` boxes of 16 rows from `row` on.
+  __device__ void tokens(const CUtensorMap* m, int k, int row, int boxes) {
     const int lane = lane_id();
     Ctl& c = *t.c;
-    const int terms = p.a.terms == 2 ? 2 : 1, cols = n * terms, quads = (cols + 3) / 4;
-    uint8_t* dst = ring + b.stage * p.stage_bytes + 2 * kTileBytes;
-    if (lane == 0) mbar_arrive_expect_tx(&c.full_b[b.stage], quads * 512);
-    __syncwarp();
-    if (lane < quads) {
-      int r[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int col = min(4 * lane + i, cols - 1);  // past the group: its last column again
-        const int tok = token_of(row0 + col / terms);
-        r[i] = tok * terms + col % terms;
-      }
-      tma_gather4(dst + lane * 512, m, k, r[0], r[1], r[2], r[3], &c.full_b[b.stage]);
-    }
-    arm_b();
-  }
-
-  // Token tile of the down phase: the group's hidden rows, in boxes of 16.
-  __device__ void hidden(const CUtensorMap* m, int k, int row0, int n) {
-    const int lane = lane_id();
-    Ctl& c = *t.c;
-    const int terms = p.a.terms == 2 ? 2 : 1, boxes = (n * terms + 15) / 16;
     uint8_t* dst = ring + b.stage * p.stage_bytes + 2 * kTileBytes;
     if (lane == 0) mbar_arrive_expect_tx(&c.full_b[b.stage], boxes * 2048);
     __syncwarp();
-    if (lane < boxes) tma_load_2d(dst + lane * 2048, m, k, row0 * terms + 16 * lane, &c.full_b[b.stage]);
+    if (lane < boxes) tma_load_2d(dst + lane * 2048, m, k, row + 16 * lane, &c.full_b[b.stage]);
     arm_b();
-  }
-
-  __device__ __forceinline__ int token_of(int r) const {
-    const int s = t.row_slot[r];
-    return r >= p.a.S * p.a.K ? s : s / p.a.K;
   }
 
   __device__ __forceinline__ void arm_b() {
@@ -669,43 +810,57 @@ struct Producer {
   }
 };
 
+__device__ __forceinline__ int up_tiles_of(const DecodeArgs& a) {
+  return a.activation == MOE_ACT_SWIGLU ? (a.h + 127) / 128 : (a.h + 255) / 256;
+}
+
 __device__ void produce(const Params& p, const Tables& t, uint8_t* ring, const Phase& up, const Phase& down,
-                        const Maps& mu, const Maps& md) {
+                        const CUtensorMap* m_in0, const CUtensorMap* m_in1, const CUtensorMap* m_out,
+                        const CUtensorMap* m_x, const CUtensorMap* m_hidden) {
   const DecodeArgs& a = p.a;
   Ctl& c = *t.c;
-  const int bk = a.terms ? 128 : 64;
-  const bool pair = a.activation == MOE_ACT_SWIGLU;
-  const int tiles = (a.h + (pair ? 127 : 255)) / (pair ? 128 : 256);
+  const int bk = a.terms ? 128 : 64, terms = a.terms == 2 ? 2 : 1;
+  const bool pair = a.activation == MOE_ACT_SWIGLU, dense = all_tokens(a.S, a.terms);
+  const int tiles = up_tiles_of(a);
   Producer pr(p, t, ring);
   bool ok = true;
-  for (int64_t s = up.lo; s < up.hi && ok;) {
+  for (int s = up.lo; s < up.hi && ok;) {
     const Unit u = unit_at(up, s);
-    const int g = u.tile / tiles, j = u.tile % tiles, slab = c.slab[g];
+    const int g = u.tile / tiles, j = u.tile - g * tiles, slab = c.slab[g];
     const int n0 = pair ? j * 128 : j * 256, n1 = pair ? n0 : n0 + 128;
+    const int row = dense ? 0 : c.first[g] * terms;
+    const int boxes = dense ? 1 : ((c.first[g + 1] - c.first[g]) * terms + 15) / 16;
     for (int k = u.k0; k < u.k1; ++k) {
-      if (!(ok = pr.weights(mu.w0, mu.w1, k * bk, n0, n1, slab))) break;
-      pr.tokens(mu.x, k * bk, c.first[g], c.first[g + 1] - c.first[g]);
+      if (!(ok = pr.weights(m_in0, m_in1, k * bk, n0, n1, slab))) break;
+      pr.tokens(m_x, k * bk, row, boxes);
     }
     s += u.k1 - u.k0;
   }
   // down: the first `ahead` steps' weights go out before the hidden rows are known to be complete
-  const int64_t steps = down.hi - down.lo;
-  const int ahead = static_cast<int>(steps < p.stages ? steps : p.stages);
-  auto down_step = [&](int64_t s, bool weights, bool tokens) {
-    const int tile = static_cast<int>(s / down.nk), k = static_cast<int>(s % down.nk);
-    const int j = tile / c.active, g = tile % c.active;
-    if (weights && !pr.weights(md.w0, md.w1, k * bk, j * 256, j * 256 + 128, c.slab[g])) return false;
-    if (tokens) pr.hidden(md.hidden, k * bk, c.first[g], c.first[g + 1] - c.first[g]);
-    return true;
-  };
-  for (int i = 0; i < ahead && ok; ++i) ok = down_step(down.lo + i, true, false);
-  if (ok) {
-    if (lane_id() == 0) ok = wait_arrivals(p, a.terms ? kCoded : kHidden, &c.abort);
-    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-    fence_proxy_async_global();
+  const int ahead = min(down.hi - down.lo, p.stages);
+  for (int pass = 0; pass < 2 && ok; ++pass) {
+    const int end = pass == 0 ? down.lo + ahead : down.hi;
+    if (pass == 1) {
+      if (lane_id() == 0) ok = wait_arrivals(p, a.terms ? kCoded : kHidden, &c.abort);
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      fence_proxy_async_global();
+    }
+    int tile = down.lo / down.nk, k = down.lo - tile * down.nk;
+    int j = tile / c.active, g = tile - j * c.active;
+    for (int s = down.lo; s < end && ok; ++s) {
+      if (pass == 0 || s >= down.lo + ahead)
+        ok = pr.weights(m_out, m_out, k * bk, j * 256, j * 256 + 128, c.slab[g]);
+      if (pass == 1 && ok)
+        pr.tokens(m_hidden, k * bk, c.first[g] * terms, ((c.first[g + 1] - c.first[g]) * terms + 15) / 16);
+      if (++k == down.nk) {
+        k = 0;
+        if (++g == c.active) {
+          g = 0;
+          ++j;
+        }
+      }
+    }
   }
-  for (int i = 0; i < ahead && ok; ++i) ok = down_step(down.lo + i, false, true);
-  for (int64_t s = down.lo + ahead; s < down.hi && ok; ++s) ok = down_step(s, true, true);
   if (!ok) {
     if (lane_id() == 0) give_up(p, &c.abort);
     pr.settle();
@@ -716,18 +871,17 @@ __device__ void produce(const Params& p, const Tables& t, uint8_t* ring, const P
 __device__ void multiply(const Params& p, const Tables& t, uint8_t* ring, const Phase& up, const Phase& down) {
   const DecodeArgs& a = p.a;
   Ctl& c = *t.c;
-  const bool pair = a.activation == MOE_ACT_SWIGLU;
-  const int tiles = (a.h + (pair ? 127 : 255)) / (pair ? 128 : 256);
-  const int terms = a.terms == 2 ? 2 : 1;
+  const int tiles = up_tiles_of(a), terms = a.terms == 2 ? 2 : 1;
+  const bool dense = all_tokens(a.S, a.terms);
   Slot at;
   int local = 0;
   bool ok = true;
   for (int ph = 0; ph < 2 && ok; ++ph) {
     const Phase& f = ph == 0 ? up : down;
-    for (int64_t s = f.lo; s < f.hi && ok; ++local) {
+    for (int s = f.lo; s < f.hi && ok; ++local) {
       const Unit u = unit_at(f, s);
       const int g = ph == 0 ? u.tile / tiles : u.tile % c.active;
-      const int n = ((c.first[g + 1] - c.first[g]) * terms + 15) & ~15;
+      const int n = ph == 0 && dense ? 16 : ((c.first[g + 1] - c.first[g]) * terms + 15) & ~15;
       const uint32_t idesc = a.terms ? idesc_e4m3_f32(128, n) : idesc_bf16_f32(128, n);
       const int acc = local & 1;
       if (!(ok = mbar_wait(&c.tempty[acc], ((local >> 1) & 1) ^ 1u, &c.abort))) break;
@@ -818,6 +972,12 @@ __device__ __forceinline__ void store_hidden(const Params& p, int r, int n, bool
   }
 }
 
+__device__ __forceinline__ void finish_hidden(const Params& p, const Tables& t, int slab, int r, int n, bool in, float v0,
+                                              float v1) {
+  const int tok = row_at(p, t, slab, r).token;
+  store_hidden(p, r, n, in, in ? hidden_value(p, t, slab, r, tok, n, v0, v1) : 0.0f);
+}
+
 // One hidden element of a tile: tile column `n` (0..127) of half `m`.
 __device__ __forceinline__ int hidden_col(bool pair, int j, int m, int n) { return pair ? j * 128 + n : j * 256 + m * 128 + n; }
 
@@ -825,19 +985,19 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
   const DecodeArgs& a = p.a;
   Ctl& c = *t.c;
   const int warp = threadIdx.x >> 5, lane = lane_id(), q = warp & 3, half = (warp - kEpiWarp0) >> 2;
-  const bool pair = a.activation == MOE_ACT_SWIGLU;
-  const int tiles = (a.h + (pair ? 127 : 255)) / (pair ? 128 : 256);
+  const bool pair = a.activation == MOE_ACT_SWIGLU, dense = all_tokens(a.S, a.terms);
+  const int tiles = up_tiles_of(a);
   const int terms = a.terms == 2 ? 2 : 1, per = 8 / terms;  // tokens per 8 columns
   const int nl = q * 32 + lane;
   bool inner_ready = a.lora.n == 0 || (a.lora.a[0] == nullptr && a.lora.a[1] == nullptr);
-  for (int64_t s = f.lo; s < f.hi; ++local) {
+  for (int s = f.lo; s < f.hi; ++local) {
     const Unit u = unit_at(f, s);
     s += u.k1 - u.k0;
-    const int g = u.tile / tiles, j = u.tile % tiles, slab = c.slab[g];
+    const int g = u.tile / tiles, j = u.tile - g * tiles, slab = c.slab[g];
     const int row0 = c.first[g], cnt = c.first[g + 1] - row0;
     const bool whole = u.k0 == 0 && u.k1 == f.nk;
-    const Join jn = join_of(f, static_cast<int64_t>(u.tile) * f.nk, static_cast<int64_t>(u.tile + 1) * f.nk);
-    float* part = partial_of(p, jn, blockIdx.x);
+    const int s0 = u.tile * f.nk;
+    float* part = partial_of(p, f, blockIdx.x, s0);
     if (!inner_ready) {
       if (!epi_wait(p, kInnerUp, &c.abort)) return false;
       inner_ready = true;
@@ -851,42 +1011,55 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
     if (epi_any(failed)) return false;
     tc_fence_after();
     const uint32_t tb = c.tmem_base + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
-    const int chunks = (cnt + per - 1) / per;
+    const int n = hidden_col(pair, j, half, nl);
+    const bool in = n < a.h;
+    const uint64_t mask = c.mask[g];
+    const int cols = dense ? a.S : cnt;  // tokens in the tile's columns
     // SwiGLU: the two halves of the warps take alternate chunks of columns, both tiles; else one tile each
-    for (int ch = pair ? half : 0; ch < chunks; ch += pair ? 2 : 1) {
+    for (int ch = pair ? half : 0; ch * per < cols; ch += pair ? 2 : 1) {
       float v0[8], v1[8];
       load_sums(tb + (pair ? 0 : half * (kAccCols / 2)) + ch * 8, terms, v0);
       if (pair) load_sums(tb + kAccCols / 2 + ch * 8, terms, v1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int tk = ch * per + i;
-        if (i >= per || tk >= cnt) break;
+        const int col = ch * per + i;
+        if (i >= per || col >= cols) break;
+        int i_row = col;
+        if (dense) {
+          if (!((mask >> col) & 1)) continue;
+          i_row = __popcll(mask & ((uint64_t(1) << col) - 1));
+        }
         if (!whole) {
-          if (pair) {
-            part[tk * 256 + nl] = v0[i];
-            part[tk * 256 + 128 + nl] = v1[i];
-          } else {
-            part[tk * 256 + half * 128 + nl] = v0[i];
-          }
+          float* o = part + i_row * 256 + nl;
+          o[pair ? 0 : half * 128] = v0[i];
+          if (pair) o[128] = v1[i];
           continue;
         }
-        const int n = hidden_col(pair, j, half, nl), r = row0 + tk;
-        const bool in = n < a.h;
-        const int tok = row_at(p, t, slab, r).token;
-        store_hidden(p, r, n, in, in ? hidden_value(p, t, slab, r, tok, n, v0[i], pair ? v1[i] : 0.0f) : 0.0f);
+        finish_hidden(p, t, slab, row0 + i_row, n, in, v0[i], pair ? v1[i] : 0.0f);
       }
     }
     tc_fence_before();
     mbar_arrive(&c.tempty[acc]);
     if (whole) continue;
-    if (!join_last(p, t, jn, 0)) continue;
-    for (int tk = pair ? half : 0; tk < cnt; tk += pair ? 2 : 1) {
-      const int n = hidden_col(pair, j, half, nl), r = row0 + tk;
-      const bool in = n < a.h;
-      const float s0 = join_sum(p, jn, tk * 256 + (pair ? 0 : half * 128) + nl);
-      const float s1 = pair ? join_sum(p, jn, tk * 256 + 128 + nl) : 0.0f;
-      const int tok = row_at(p, t, slab, r).token;
-      store_hidden(p, r, n, in, in ? hidden_value(p, t, slab, r, tok, n, s0, s1) : 0.0f);
+    const int c0 = f.part_of(s0), c1 = f.part_of(s0 + f.nk - 1);
+    if (!join_last(p, t, c0, c1)) continue;
+    // rows four at a time, so that their loads are in flight together
+    const int step = pair ? 8 : 4;
+    for (int i0 = pair ? half * 4 : 0; i0 < cnt; i0 += step) {
+      float v0[4] = {0.f, 0.f, 0.f, 0.f}, v1[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int cc = c0; cc <= c1; ++cc) {
+        const float* src = partial_of(p, f, cc, s0) + i0 * 256 + nl + (pair ? 0 : half * 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i0 + i < cnt) {
+            v0[i] += __ldcg(src + i * 256);
+            if (pair) v1[i] += __ldcg(src + i * 256 + 128);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i < cnt) finish_hidden(p, t, slab, row0 + i0 + i, n, in, v0[i], v1[i]);
     }
   }
   return true;
@@ -899,18 +1072,16 @@ __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, 
   const int terms = a.terms == 2 ? 2 : 1, per = 8 / terms;
   const int nl = half * 128 + q * 32 + lane;  // this thread's column of the tile
   const int slabs = a.E + a.num_shared;
-  const int64_t tile_steps = static_cast<int64_t>(c.active) * f.nk;  // steps of one output tile, all groups
+  const int tile_steps = c.active * f.nk;  // steps of one output tile, all groups
   bool inner_ready = a.lora.n == 0 || a.lora.a[2] == nullptr;
-  auto* y = static_cast<__nv_bfloat16*>(a.y);
-  for (int64_t s = f.lo; s < f.hi;) {
-    const int64_t s0 = s / tile_steps * tile_steps, s1 = s0 + tile_steps;
-    const int j = static_cast<int>(s / tile_steps), n = j * 256 + nl;
+  for (int s = f.lo; s < f.hi;) {
+    const int j = s / tile_steps, s0 = j * tile_steps, s1 = s0 + tile_steps, n = j * 256 + nl;
     const bool in = n < a.d;
     for (int tk = 0; tk < a.S; ++tk) t.y[tk * 256 + nl] = 0.0f;
     for (; s < f.hi && s < s1; ++local) {
       const Unit u = unit_at(f, s);
       s += u.k1 - u.k0;
-      const int g = u.tile % c.active, slab = c.slab[g], row0 = c.first[g], cnt = c.first[g + 1] - row0;
+      const int g = u.tile - j * c.active, slab = c.slab[g], row0 = c.first[g], cnt = c.first[g + 1] - row0;
       if (!inner_ready && u.k0 == 0) {
         if (!epi_wait(p, kCoded, &c.abort)) return false;
         inner_ready = true;
@@ -950,21 +1121,39 @@ __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, 
       tc_fence_before();
       mbar_arrive(&c.tempty[acc]);
     }
-    const Join jn = join_of(f, s0, s1);
-    if (jn.c0 == jn.c1) {
+    if (f.lo <= s0 && f.hi >= s1) {  // the whole tile: final
+      auto* y = static_cast<__nv_bfloat16*>(a.y);
       for (int tk = 0; tk < a.S; ++tk)
         if (in) y[static_cast<int64_t>(tk) * a.d + n] = __float2bfloat16_rn(t.y[tk * 256 + nl]);
       continue;
     }
-    float* part = partial_of(p, jn, blockIdx.x);
+    float* part = partial_of(p, f, blockIdx.x, s0);
     for (int tk = 0; tk < a.S; ++tk) part[tk * 256 + nl] = t.y[tk * 256 + nl];
-    if (!join_last(p, t, jn, 1)) continue;
-    for (int tk = 0; tk < a.S; ++tk) {
-      const float v = join_sum(p, jn, tk * 256 + nl);
-      if (in) y[static_cast<int64_t>(tk) * a.d + n] = __float2bfloat16_rn(v);
-    }
   }
   return true;
+}
+
+// y = the partial tiles' sums, four columns per thread of the grid.
+__device__ void sum_partials(const Params& p, const Tables& t, const Phase& f) {
+  const DecodeArgs& a = p.a;
+  const int quads = a.d / 4, tile_steps = t.c->active * f.nk;
+  auto* y = static_cast<__nv_bfloat16*>(a.y);
+  for (int i = blockIdx.x * kEpiThreads + threadIdx.x - 32 * kEpiWarp0; i < a.S * quads; i += gridDim.x * kEpiThreads) {
+    const int tk = i / quads, n = (i - tk * quads) * 4, s0 = n / 256 * tile_steps;
+    const int c0 = f.part_of(s0), c1 = f.part_of(s0 + tile_steps - 1);
+    if (c0 == c1) continue;  // stored by its CTA
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const float4 q = __ldcg(reinterpret_cast<const float4*>(partial_of(p, f, c, s0) + tk * 256 + n % 256));
+      v.x += q.x;
+      v.y += q.y;
+      v.z += q.z;
+      v.w += q.w;
+    }
+    *reinterpret_cast<uint2*>(y + static_cast<int64_t>(tk) * a.d + n) =
+        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  }
 }
 
 __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, const Phase& down) {
@@ -986,7 +1175,10 @@ __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, cons
     epi_arrive(p, kCoded);
     if (a.terms && !epi_wait(p, kCoded, &c.abort)) return;  // the codes' row scales
   }
-  epilogue_down(p, t, down, local);
+  if (!epilogue_down(p, t, down, local)) return;
+  epi_arrive(p, kSummed);
+  if (!epi_wait(p, kSummed, &c.abort)) return;
+  sum_partials(p, t, down);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -999,6 +1191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Tables t;
   uint8_t* at = ring + p.ring_bytes;
   t.c = reinterpret_cast<Ctl*>(at);
+  t.scratch = reinterpret_cast<Scratch*>(ring);
   at += (sizeof(Ctl) + 15) & ~size_t(15);
   t.y = reinterpret_cast<float*>(at);
   at += static_cast<size_t>(a.S) * 256 * 4;
@@ -1031,17 +1224,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  route_phase(p);
-  if (grid_barrier(p, c, kRouted)) {
-    tables_phase(p, t);
+  route_phase(p, *t.scratch);
+  if (grid_barrier(p, c, kRouted) && tables_phase(p, t)) {
     const bool pair = a.activation == MOE_ACT_SWIGLU;
     const int bk = a.terms ? 128 : 64;
-    const int up_tiles = (a.h + (pair ? 127 : 255)) / (pair ? 128 : 256);
-    const Phase up = phase_of(c.active * up_tiles, (a.d + bk - 1) / bk);
+    const Phase up = phase_of(c.active * up_tiles_of(a), (a.d + bk - 1) / bk);
     const Phase down = phase_of(c.active * ((a.d + 255) / 256), (a.h + bk - 1) / bk);
     if (warp == 0)
-      produce(p, t, ring, up, down, Maps{&m_in0, pair ? &m_in1 : &m_in0, &m_x, nullptr},
-              Maps{&m_out, &m_out, nullptr, &m_hidden});
+      produce(p, t, ring, up, down, &m_in0, pair ? &m_in1 : &m_in0, &m_out, &m_x, &m_hidden);
     else if (warp == 1 && lane_id() == 0)
       multiply(p, t, ring, up, down);
     else if (warp >= kEpiWarp0)
@@ -1077,9 +1267,12 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   char* ws = static_cast<char*>(a.ws);
   Params p;
   p.a = a;
-  p.logits = reinterpret_cast<float*>(ws + L.logits);
+  p.logits = reinterpret_cast<double*>(ws + L.logits);
+  p.idx = reinterpret_cast<int*>(ws + L.idx);
+  p.gate = reinterpret_cast<float*>(ws + L.gate);
   p.xq = reinterpret_cast<uint8_t*>(ws + L.xq);
   p.xs = reinterpret_cast<float*>(ws + L.xs);
+  p.xp = reinterpret_cast<uint8_t*>(ws + L.xp);
   p.hidden = reinterpret_cast<__nv_bfloat16*>(ws + L.hidden);
   p.amax = reinterpret_cast<uint32_t*>(ws + L.amax);
   p.hq = reinterpret_cast<uint8_t*>(ws + L.hq);
@@ -1099,14 +1292,21 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   if (p.stages < 2) return cudaErrorInvalidValue;
   p.ring_bytes = p.stages * p.stage_bytes;
   const int slabs = a.E + a.num_shared;
+  // steps are counted in 32 bits (two of them added at most)
+  const int64_t bk = a.terms ? 128 : 64;
+  if (slabs * ((a.h + 127) / 128) * ((a.d + bk - 1) / bk) > (1 << 30) ||
+      slabs * ((a.d + 255) / 256) * ((a.h + bk - 1) / bk) > (1 << 30))
+    return cudaErrorInvalidValue;
   const int64_t rows = static_cast<int64_t>(a.S) * (a.K + a.num_shared);
   CUtensorMap in0, in1, out, mx, mh;
   if (!gemm::make_slab_map(&in0, a.w_in[0], slabs, a.h, a.d, eb) || !gemm::make_slab_map(&out, a.w_out, slabs, a.d, a.h, eb))
     return cudaErrorInvalidValue;
   in1 = in0;
   if (a.w_in[1] != nullptr && !gemm::make_slab_map(&in1, a.w_in[1], slabs, a.h, a.d, eb)) return cudaErrorInvalidValue;
-  // tokens: rows gathered one by one; hidden rows: boxes of 16
-  if (!gemm::make_map(&mx, a.terms ? static_cast<const void*>(p.xq) : a.x, static_cast<int64_t>(a.S) * terms, a.d, 1, eb) ||
+  // token rows: all of x (or its codes), or the rows copied group by group; boxes of 16 rows
+  const bool dense = all_tokens(a.S, a.terms);
+  const void* xrows = !dense ? p.xp : a.terms ? static_cast<const void*>(p.xq) : a.x;
+  if (!gemm::make_map(&mx, xrows, (dense ? a.S : rows) * terms, a.d, 16, eb) ||
       !gemm::make_map(&mh, a.terms ? static_cast<const void*>(p.hq) : p.hidden, rows * terms, a.h, 16, eb))
     return cudaErrorInvalidValue;
   const int grid = a.num_sms < kDecodeMaxCtas ? a.num_sms : kDecodeMaxCtas;
