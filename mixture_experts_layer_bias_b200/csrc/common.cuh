@@ -175,14 +175,26 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
-// 3-D tiled load (c2 the outermost coordinate): a box of one slab's rows, rows
-// past the slab's end read as zero.
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m, int c0, int c1, int c2,
-                                            uint64_t* bar) {
+// L2 eviction policies for loads with a cache hint.
+__device__ __forceinline__ uint64_t l2_evict_first() {
+  uint64_t h;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(h));
+  return h;
+}
+__device__ __forceinline__ uint64_t l2_evict_normal() {
+  uint64_t h;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(h));
+  return h;
+}
+
+// 3-D tiled load (c2 the outermost coordinate) with an L2 policy: a box of one
+// slab's rows, rows past the slab's end read as zero.
+__device__ __forceinline__ void tma_load_3d_hint(void* smem_dst, const CUtensorMap* m, int c0, int c1, int c2,
+                                                 uint64_t* bar, uint64_t hint) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-      "[%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(hint)
       : "memory");
 }
 

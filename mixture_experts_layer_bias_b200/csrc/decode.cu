@@ -56,6 +56,7 @@
 // waits then run out too.
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -147,6 +148,7 @@ struct Params {
   StatusBlock* status;
   GridSync* sync;
   int stages, stage_bytes, ring_bytes;
+  int stream_weights;  // weights leave L2 first
 };
 
 // Shared-memory control block of one CTA; the selection's arrays follow it.
@@ -175,22 +177,22 @@ struct Scratch {
   uint64_t key[kThreads];   // ordered keys
   double score[kThreads];   // gate sources
   double sum[kThreads];     // logits: warp sums; selection: group scores, then the picks' gate sources
+  int idx[MOE_DECODE_MAX_TOKENS * 32];     // [S][K]
+  float gate[MOE_DECODE_MAX_TOKENS * 32];  // [S][K]
 };
 
 struct Tables {
   Ctl* c;
   Scratch* scratch;
-  float* gate;         // [S][K]
-  int* idx;            // [S][K]
-  uint16_t* row_slot;  // row -> slot t*K + k (shared rows: token)
   float* y;            // [S][256]: the down phase's sums of one tile, column n owned by one thread
+  float* row_gate;     // row -> its gate
+  float* row_scale;    // E4M3: row -> its codes' scale (tokens, then hidden rows)
+  uint16_t* row_tok;   // row -> its token
 };
 
 size_t tables_bytes(int S, int K, int ns) {
-  size_t b = (sizeof(Ctl) + 15) & ~size_t(15);
-  b += static_cast<size_t>(S) * K * 8;
-  b += (static_cast<size_t>(S) * (K + ns) * 2 + 15) & ~size_t(15);
-  return b + static_cast<size_t>(S) * 256 * 4;
+  const size_t rows = static_cast<size_t>(S) * (K + ns);
+  return ((sizeof(Ctl) + 15) & ~size_t(15)) + static_cast<size_t>(S) * 256 * 4 + ((rows * 10 + 15) & ~size_t(15));
 }
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
@@ -395,7 +397,7 @@ __device__ void select_tokens(const Params& p, Scratch& c, int t0, int n, int wi
   double score = 0.0, key = kNegInf;
   if (in) {
     const double l = __ldcg(p.logits + static_cast<int64_t>(t0 + j) * a.E + e);
-    score = a.score_fn == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-l)) : l / static_cast<double>(a.tau);
+    score = a.score_fn == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-l)) : (a.tau == 1.0f ? l : l / static_cast<double>(a.tau));
     key = a.sel_bias != nullptr ? score + static_cast<double>(__ldg(a.sel_bias + e)) : score;
     if (isnan(key)) key = kNegInf;
     c.score[tid] = score;
@@ -487,27 +489,27 @@ __device__ void select_tokens(const Params& p, Scratch& c, int t0, int n, int wi
 __device__ bool tables_phase(const Params& p, const Tables& t) {
   const DecodeArgs& a = p.a;
   Ctl& c = *t.c;
+  Scratch& sc = *t.scratch;
   const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
   const int slots = a.S * a.K, slabs = a.E + a.num_shared;
   const int width = select_width(a.E), per = kThreads / width, rounds = (a.S + per - 1) / per;
   for (int i = tid; i < slabs; i += kThreads) c.tokens_of[i] = 0;
   if (rounds <= 2) {
     for (int r = 0; r < rounds; ++r)
-      select_tokens(p, *t.scratch, r * per, min(per, a.S - r * per), width, t.idx, t.gate, blockIdx.x == 0);
+      select_tokens(p, sc, r * per, min(per, a.S - r * per), width, sc.idx, sc.gate, blockIdx.x == 0);
   } else {
     for (int r = blockIdx.x; r < rounds; r += gridDim.x)
-      select_tokens(p, *t.scratch, r * per, min(per, a.S - r * per), width, p.idx, p.gate, true);
+      select_tokens(p, sc, r * per, min(per, a.S - r * per), width, p.idx, p.gate, true);
     if (!grid_barrier(p, c, kSelected)) return false;
     for (int i = tid; i < slots; i += kThreads) {
-      t.idx[i] = __ldcg(p.idx + i);
-      t.gate[i] = __ldcg(p.gate + i);
+      sc.idx[i] = __ldcg(p.idx + i);
+      sc.gate[i] = __ldcg(p.gate + i);
     }
     __syncthreads();
   }
-  fence_proxy_async_smem();  // the scratch lies where the first copies land
   // an expert's tokens as a 64-bit mask: its rows are the set bits in token order
   for (int i = tid; i < slots; i += kThreads)
-    atomicOr(reinterpret_cast<unsigned long long*>(c.tokens_of + t.idx[i]), 1ull << (i / a.K));
+    atomicOr(reinterpret_cast<unsigned long long*>(c.tokens_of + sc.idx[i]), 1ull << (i / a.K));
   if (tid == 0 && a.num_shared) c.tokens_of[a.E] = a.S == 64 ? ~uint64_t(0) : (uint64_t(1) << a.S) - 1;
   if (a.lora.n > 0) {
     for (int i = tid; i < a.S; i += kThreads) {
@@ -547,25 +549,29 @@ __device__ bool tables_phase(const Params& p, const Tables& t) {
     c.first[all >> 16] = all & 0xFFFF;
   }
   __syncthreads();
-  for (int i = tid; i < slots; i += kThreads) {
-    const int e = t.idx[i], tok = i / a.K;
-    t.row_slot[c.row0[e] + __popcll(c.tokens_of[e] & ((uint64_t(1) << tok) - 1))] = static_cast<uint16_t>(i);
+  for (int i = tid; i < slots + a.S * a.num_shared; i += kThreads) {
+    const bool shared = i >= slots;
+    const int tok = shared ? i - slots : i / a.K;
+    const int e = shared ? a.E : sc.idx[i];
+    const int r = c.row0[e] + __popcll(c.tokens_of[e] & ((uint64_t(1) << tok) - 1));
+    t.row_tok[r] = static_cast<uint16_t>(tok);
+    t.row_gate[r] = shared ? 1.0f : sc.gate[i];
+    if (a.terms) t.row_scale[r] = __ldcg(p.xs + tok);
   }
-  if (a.num_shared)
-    for (int i = tid; i < a.S; i += kThreads) t.row_slot[slots + i] = static_cast<uint16_t>(i);
   if (blockIdx.x == 0) {
     if (a.counts != nullptr && tid < a.E) a.counts[tid] = count;
     for (int i = tid; i < slots; i += kThreads) {
-      if (a.topk_idx != nullptr) a.topk_idx[i] = t.idx[i];
-      if (a.topk_w != nullptr) a.topk_w[i] = t.gate[i];
+      if (a.topk_idx != nullptr) a.topk_idx[i] = sc.idx[i];
+      if (a.topk_w != nullptr) a.topk_w[i] = sc.gate[i];
     }
   }
+  fence_proxy_async_smem();  // the scratch lies where the first copies land
   __syncthreads();
   if (all_tokens(a.S, a.terms)) return true;
   // token rows or codes, group by group: a warp per row
   const int rows = slots + a.S * a.num_shared, bytes = a.d * (a.terms ? a.terms : 2);
   for (int r = blockIdx.x + gridDim.x * warp; r < rows; r += gridDim.x * kWarps) {
-    const int tok = r < slots ? t.row_slot[r] / a.K : t.row_slot[r];
+    const int tok = t.row_tok[r];
     const auto* src = reinterpret_cast<const uint4*>(
         (a.terms ? p.xq : static_cast<const uint8_t*>(a.x)) + static_cast<int64_t>(tok) * bytes);
     auto* dst = reinterpret_cast<uint4*>(p.xp + static_cast<int64_t>(r) * bytes);
@@ -580,18 +586,6 @@ __device__ bool tables_phase(const Params& p, const Tables& t) {
     }
   }
   return grid_barrier(p, c, kPacked);
-}
-
-struct Row {
-  int token;
-  float gate;
-};
-
-// The row `r` of an active group with slab `slab`.
-__device__ __forceinline__ Row row_at(const Params& p, const Tables& t, int slab, int r) {
-  const int s = t.row_slot[r];
-  if (slab == p.a.E) return Row{s, 1.0f};
-  return Row{s / p.a.K, t.gate[s]};
 }
 
 __device__ __forceinline__ int group_of_row(const Ctl& c, int r) {
@@ -619,7 +613,7 @@ __device__ void adapter_inner(const Params& p, const Tables& t, int m0, int nm) 
     const int j = i % blocks * 8, m = m0 + (i / blocks) % nm, r = i / (blocks * nm);
     if (l.a[m] == nullptr) continue;
     const int slab = t.c->slab[group_of_row(*t.c, r)];
-    const int token = row_at(p, t, slab, r).token, ad = t.c->adapter[token];
+    const int token = t.row_tok[r], ad = t.c->adapter[token];
     if (ad < 0) continue;
     const auto* w = static_cast<const __nv_bfloat16*>(l.a[m]) + ((static_cast<int64_t>(ad) * slabs + slab) * l.r + j) * n;
     const __nv_bfloat16* src = m0 == 2 ? p.hidden + static_cast<int64_t>(r) * n
@@ -652,26 +646,27 @@ __device__ void adapter_inner(const Params& p, const Tables& t, int m0, int nm) 
   }
 }
 
-// Epilogue warps: the hidden rows' codes from their maxima, a warp per 1024 columns of a row.
+// Epilogue warps: the hidden rows' codes from their maxima, a warp per 512 columns of a row.
 __device__ void code_hidden(const Params& p, const Tables& t) {
   const DecodeArgs& a = p.a;
-  const int rows = t.c->first[t.c->active], pieces = (a.h + 1023) / 1024;
+  const int rows = t.c->first[t.c->active], pieces = (a.h + 511) / 512;
   const int warp = (threadIdx.x >> 5) - kEpiWarp0;
   for (int i = blockIdx.x + gridDim.x * warp; i < rows * pieces; i += gridDim.x * (kEpiThreads / 32)) {
-    const int r = i / pieces, c0 = (i % pieces) * 1024 + lane_id() * 8;
-    const uint32_t bits = __ldcg(p.amax + r);
-    float s, m;
-    coding::row_scale(a.terms, __uint_as_float(bits << 16), bits > 0x7F80u, bits >= 0x7F80u, s, m);
+    const int r = i / pieces, piece = i - r * pieces, c0 = piece * 512 + lane_id() * 8, c1 = c0 + 256;
     const __nv_bfloat16* src = p.hidden + static_cast<int64_t>(r) * a.h;
     uint8_t* dst = p.hq + static_cast<int64_t>(r) * a.terms * a.h;
-    uint4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      v[k] = c0 + 256 * k < a.h ? __ldcg(reinterpret_cast<const uint4*>(src + c0 + 256 * k)) : make_uint4(0, 0, 0, 0);
+    const uint32_t bits = __ldcg(p.amax + r);
+    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+    if (c0 < a.h) v0 = __ldcg(reinterpret_cast<const uint4*>(src + c0));
+    if (c1 < a.h) v1 = __ldcg(reinterpret_cast<const uint4*>(src + c1));
+    float s, m;
+    coding::row_scale(a.terms, __uint_as_float(bits << 16), bits > 0x7F80u, bits >= 0x7F80u, s, m);
 #pragma unroll 1
-    for (int k = 0; k < 4; ++k)
-      if (c0 + 256 * k < a.h) coding::code_piece(v[k], dst, a.h, c0 + 256 * k, a.terms, s, m);
-    if (i % pieces == 0 && lane_id() == 0) p.hs[r] = s;
+    for (int k = 0; k < 2; ++k) {
+      const int col = k == 0 ? c0 : c1;
+      if (col < a.h) coding::code_piece(k == 0 ? v0 : v1, dst, a.h, col, a.terms, s, m);
+    }
+    if (piece == 0 && lane_id() == 0) p.hs[r] = s;
   }
 }
 
@@ -758,9 +753,10 @@ struct Producer {
   const Tables& t;
   uint8_t* ring;
   Slot w, b;
+  uint64_t hint;
   uint32_t armed_w = 0, armed_b = 0, round_w = 0, round_b = 0;  // barriers armed, for an abort
 
-  __device__ Producer(const Params& p_, const Tables& t_, uint8_t* ring_) : p(p_), t(t_), ring(ring_) {}
+  __device__ Producer(const Params& p_, const Tables& t_, uint8_t* ring_) : p(p_), t(t_), ring(ring_) { hint = p.stream_weights ? l2_evict_first() : l2_evict_normal(); }
 
   // Two weight tiles: rows n0 of slab `slab` of w0, and rows n1 of w1.
   __device__ bool weights(const CUtensorMap* w0, const CUtensorMap* w1, int k, int n0, int n1, int slab) {
@@ -773,8 +769,8 @@ struct Producer {
     uint8_t* st = ring + w.stage * p.stage_bytes;
     if (lane == 0) {
       mbar_arrive_expect_tx(&c.full_w[w.stage], 2 * kTileBytes);
-      tma_load_3d(st, w0, k, n0, slab, &c.full_w[w.stage]);
-      tma_load_3d(st + kTileBytes, w1, k, n1, slab, &c.full_w[w.stage]);
+      tma_load_3d_hint(st, w0, k, n0, slab, &c.full_w[w.stage], hint);
+      tma_load_3d_hint(st + kTileBytes, w1, k, n1, slab, &c.full_w[w.stage], hint);
     }
     armed_w |= 1u << w.stage;
     round_w = (round_w & ~(1u << w.stage)) | (w.round << w.stage);
@@ -931,20 +927,20 @@ __device__ __forceinline__ void load_sums(uint32_t taddr, int terms, float (&v)[
   }
 }
 
-// Final sums of hidden column n of row r (token `tok`): scales, adapters, bias,
-// activation.  v0, v1: gate and up (SwiGLU), or v0 alone.
-__device__ __forceinline__ float hidden_value(const Params& p, const Tables& t, int slab, int r, int tok, int n,
-                                              float v0, float v1) {
+// Final sums of hidden column n of row r: scales (cs0, cs1: the column's, 1
+// without E4M3 weights), adapters, bias, activation.  v0, v1: gate and up
+// (SwiGLU), or v0 alone.
+__device__ __forceinline__ float hidden_value(const Params& p, const Tables& t, int slab, int r, int n, float cs0,
+                                              float cs1, float bias, float v0, float v1) {
   const DecodeArgs& a = p.a;
-  const int64_t ch = static_cast<int64_t>(slab) * a.h + n;
   const bool pair = a.activation == MOE_ACT_SWIGLU;
   if (a.terms) {
-    const float rs = __ldcg(p.xs + tok);
-    v0 *= rs * __ldg(a.s_in[0] + ch);
-    v1 *= rs * __ldg(a.s_in[1] + ch);
+    const float rs = t.row_scale[r];
+    v0 *= rs * cs0;
+    v1 *= rs * cs1;
   }
   if (a.lora.n > 0) {
-    const int ad = t.c->adapter[tok], slabs = a.E + a.num_shared;
+    const int ad = t.c->adapter[t.row_tok[r]], slabs = a.E + a.num_shared;
     if (ad >= 0) {
       const float* u = p.u_in + static_cast<int64_t>(r) * 2 * a.lora.r;
       if (pair) {
@@ -956,7 +952,7 @@ __device__ __forceinline__ float hidden_value(const Params& p, const Tables& t, 
     }
   }
   if (pair) return v0 / (1.0f + __expf(-v0)) * v1;
-  const float z = v0 + __ldg(a.b_in + ch);
+  const float z = v0 + bias;
   return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
 }
 
@@ -970,12 +966,6 @@ __device__ __forceinline__ void store_hidden(const Params& p, int r, int n, bool
     const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, bits);
     if (lane_id() == 0) atomicMax(p.amax + r, m);
   }
-}
-
-__device__ __forceinline__ void finish_hidden(const Params& p, const Tables& t, int slab, int r, int n, bool in, float v0,
-                                              float v1) {
-  const int tok = row_at(p, t, slab, r).token;
-  store_hidden(p, r, n, in, in ? hidden_value(p, t, slab, r, tok, n, v0, v1) : 0.0f);
 }
 
 // One hidden element of a tile: tile column `n` (0..127) of half `m`.
@@ -1002,6 +992,20 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
       if (!epi_wait(p, kInnerUp, &c.abort)) return false;
       inner_ready = true;
     }
+    const int n = hidden_col(pair, j, half, nl);
+    const bool in = n < a.h;
+    float cs0 = 1.0f, cs1 = 1.0f, bias = 0.0f;  // the column's scales or bias, loaded while the sums are made
+    if (in) {
+      const int64_t ch = static_cast<int64_t>(slab) * a.h + n;
+      if (a.terms) {
+        cs0 = __ldg(a.s_in[0] + ch);
+        cs1 = __ldg(a.s_in[1] + ch);
+      }
+      if (!pair) bias = __ldg(a.b_in + ch);
+    }
+    auto finish = [&](int r, float v0, float v1) {
+      store_hidden(p, r, n, in, in ? hidden_value(p, t, slab, r, n, cs0, cs1, bias, v0, v1) : 0.0f);
+    };
     const int acc = local & 1;
     bool failed = false;
     if (!mbar_wait(&c.tfull[acc], (local >> 1) & 1, &c.abort)) {
@@ -1011,8 +1015,6 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
     if (epi_any(failed)) return false;
     tc_fence_after();
     const uint32_t tb = c.tmem_base + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
-    const int n = hidden_col(pair, j, half, nl);
-    const bool in = n < a.h;
     const uint64_t mask = c.mask[g];
     const int cols = dense ? a.S : cnt;  // tokens in the tile's columns
     // SwiGLU: the two halves of the warps take alternate chunks of columns, both tiles; else one tile each
@@ -1035,7 +1037,7 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
           if (pair) o[128] = v1[i];
           continue;
         }
-        finish_hidden(p, t, slab, row0 + i_row, n, in, v0[i], pair ? v1[i] : 0.0f);
+        finish(row0 + i_row, v0[i], pair ? v1[i] : 0.0f);
       }
     }
     tc_fence_before();
@@ -1059,7 +1061,7 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i0 + i < cnt) finish_hidden(p, t, slab, row0 + i0 + i, n, in, v0[i], v1[i]);
+        if (i0 + i < cnt) finish(row0 + i0 + i, v0[i], v1[i]);
     }
   }
   return true;
@@ -1086,6 +1088,9 @@ __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, 
         if (!epi_wait(p, kCoded, &c.abort)) return false;
         inner_ready = true;
       }
+      const int64_t och = static_cast<int64_t>(slab) * a.d + n;
+      const float cs = a.terms && in ? __ldg(a.s_out + och) : 1.0f;
+      const float bias = a.b_out != nullptr && in && u.k0 == 0 ? __ldg(a.b_out + och) : 0.0f;
       const int acc = local & 1;
       bool failed = false;
       if (!mbar_wait(&c.tfull[acc], (local >> 1) & 1, &c.abort)) {
@@ -1095,9 +1100,6 @@ __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, 
       if (epi_any(failed)) return false;
       tc_fence_after();
       const uint32_t tb = c.tmem_base + acc * kAccCols + half * (kAccCols / 2) + (static_cast<uint32_t>(q * 32) << 16);
-      const int64_t och = static_cast<int64_t>(slab) * a.d + n;
-      const float cs = a.terms && in ? __ldg(a.s_out + och) : 1.0f;
-      const float bias = a.b_out != nullptr && in && u.k0 == 0 ? __ldg(a.b_out + och) : 0.0f;
       for (int ch = 0; ch * per < cnt; ++ch) {
         float v[8];
         load_sums(tb + ch * 8, terms, v);
@@ -1106,16 +1108,16 @@ __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, 
           const int tk = ch * per + i;
           if (i >= per || tk >= cnt) break;
           const int r = row0 + tk;
-          const Row row = row_at(p, t, slab, r);
+          const int tok = t.row_tok[r];
           float o = v[i];
-          if (a.terms) o *= __ldcg(p.hs + r) * cs;
+          if (a.terms) o *= t.row_scale[r] * cs;
           if (u.k0 == 0) {
             o += bias;
-            if (in && a.lora.n > 0 && a.lora.a[2] != nullptr && c.adapter[row.token] >= 0)
-              o += adapter_delta(a.lora, 2, slabs, c.adapter[row.token], slab, a.d, n,
+            if (in && a.lora.n > 0 && a.lora.a[2] != nullptr && c.adapter[tok] >= 0)
+              o += adapter_delta(a.lora, 2, slabs, c.adapter[tok], slab, a.d, n,
                                  p.u_out + static_cast<int64_t>(r) * a.lora.r);
           }
-          t.y[row.token * 256 + nl] += row.gate * o;
+          t.y[tok * 256 + nl] += t.row_gate[r] * o;
         }
       }
       tc_fence_before();
@@ -1143,7 +1145,7 @@ __device__ void sum_partials(const Params& p, const Tables& t, const Phase& f) {
     const int c0 = f.part_of(s0), c1 = f.part_of(s0 + tile_steps - 1);
     if (c0 == c1) continue;  // stored by its CTA
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int c = c0; c <= c1; ++c) {
       const float4 q = __ldcg(reinterpret_cast<const float4*>(partial_of(p, f, c, s0) + tk * 256 + n % 256));
       v.x += q.x;
@@ -1173,7 +1175,12 @@ __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, cons
     if (a.terms) code_hidden(p, t);
     if (inner_down) adapter_inner(p, t, 2, 1);
     epi_arrive(p, kCoded);
-    if (a.terms && !epi_wait(p, kCoded, &c.abort)) return;  // the codes' row scales
+    if (a.terms) {  // the hidden rows' scales
+      if (!epi_wait(p, kCoded, &c.abort)) return;
+      for (int r = threadIdx.x - 32 * kEpiWarp0; r < c.first[c.active]; r += kEpiThreads)
+        t.row_scale[r] = __ldcg(p.hs + r);
+      epi_any(false);
+    }
   }
   if (!epilogue_down(p, t, down, local)) return;
   epi_arrive(p, kSummed);
@@ -1195,11 +1202,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   at += (sizeof(Ctl) + 15) & ~size_t(15);
   t.y = reinterpret_cast<float*>(at);
   at += static_cast<size_t>(a.S) * 256 * 4;
-  t.gate = reinterpret_cast<float*>(at);
-  at += static_cast<size_t>(a.S) * a.K * 4;
-  t.idx = reinterpret_cast<int*>(at);
-  at += static_cast<size_t>(a.S) * a.K * 4;
-  t.row_slot = reinterpret_cast<uint16_t*>(at);
+  const int rows = a.S * (a.K + a.num_shared);
+  t.row_gate = reinterpret_cast<float*>(at);
+  t.row_scale = t.row_gate + rows;
+  t.row_tok = reinterpret_cast<uint16_t*>(t.row_scale + rows);
   Ctl& c = *t.c;
   const int warp = threadIdx.x >> 5;
   if (warp == 1) {
@@ -1289,7 +1295,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   const size_t fixed = 1024 + tables_bytes(a.S, a.K, a.num_shared);
   p.stages = static_cast<int>((kSmemLimit - fixed) / p.stage_bytes);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  if (p.stages < 2) return cudaErrorInvalidValue;
+  if (p.stages < 2 || p.stages * p.stage_bytes < static_cast<int>(sizeof(Scratch))) return cudaErrorInvalidValue;
   p.ring_bytes = p.stages * p.stage_bytes;
   const int slabs = a.E + a.num_shared;
   // steps are counted in 32 bits (two of them added at most)
@@ -1309,6 +1315,12 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   if (!gemm::make_map(&mx, xrows, (dense ? a.S : rows) * terms, a.d, 16, eb) ||
       !gemm::make_map(&mh, a.terms ? static_cast<const void*>(p.hq) : p.hidden, rows * terms, a.h, 16, eb))
     return cudaErrorInvalidValue;
+  // Each weight byte is read once per call.  Where the touched experts exceed half of the 126 MB L2, their lines are
+  // marked to leave first, which keeps the kernel's code, the router weights and the activations there between calls;
+  // a smaller layer may find its weights in L2 the next time.
+  const int64_t touched = std::min<int64_t>(a.E, static_cast<int64_t>(a.S) * a.K) + a.num_shared;
+  const int mats = a.activation == MOE_ACT_SWIGLU ? 3 : 2;
+  p.stream_weights = touched * mats * a.h * a.d * eb > (int64_t(63) << 20);
   const int grid = a.num_sms < kDecodeMaxCtas ? a.num_sms : kDecodeMaxCtas;
   void* args[] = {&in0, &in1, &out, &mx, &mh, &p};
   return cudaLaunchCooperativeKernel(reinterpret_cast<void*>(decode_kernel), dim3(grid), dim3(kThreads), args,
