@@ -42,6 +42,8 @@ struct RouteArgs {
   float* score_out;         // optional [S][E]: gate sources (logits or sigmoid scores), with cand_key_out
 };
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
+// x W_r^T alone, into logits_scratch.
+cudaError_t launch_router_logits(const RouteArgs& a, cudaStream_t stream);
 
 // --- over-capacity re-routing ------------------------------------------------
 // Excess slots (row_of_slot >= E*C after a capacity-bounded permutation) move,

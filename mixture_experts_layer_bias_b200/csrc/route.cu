@@ -444,6 +444,42 @@ cudaError_t launch_route_rows_f32(const RouteArgs& a, const SelectParams& sp, cu
 
 }  // namespace
 
+// x W_r^T into logits_scratch (the router bias is added by the selection).
+cudaError_t launch_router_logits(const RouteArgs& a, cudaStream_t stream) {
+  // bf16: one dense GEMM on the tensor cores (fp32 accumulate and output, which
+  // it stores four columns at a time: E a multiple of 4)
+  if (a.act_dtype == MOE_BF16 && a.d % 8 == 0 && a.E % 4 == 0) {
+    GemmArgs g{};
+    g.epilogue = EPI_NONE;
+    g.groups = nullptr;
+    g.num_groups = 1;
+    g.shared_slab = -1;
+    g.a = a.x;
+    g.a_rows = a.S;
+    g.b0 = a.w_router;
+    g.b_rows = a.E;
+    g.n_per_slab = a.E;
+    g.N = a.E;
+    g.K = a.d;
+    g.out = a.logits_scratch;
+    g.out_rows = a.S;
+    g.out_f32 = 1;
+    g.max_total_rows = a.S;
+    g.max_group_rows = a.S;
+    g.status = a.status;
+    return launch_grouped_gemm_tc(g, a.num_sms, stream);
+  }
+  dim3 grid((a.S + 31) / 32, (a.E + 63) / 64);
+  if (a.act_dtype == MOE_BF16)
+    logits_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a.S, a.d, a.E, static_cast<const __nv_bfloat16*>(a.x),
+                                                            static_cast<const __nv_bfloat16*>(a.w_router),
+                                                            a.logits_scratch);
+  else
+    logits_kernel<float><<<grid, 256, 0, stream>>>(a.S, a.d, a.E, static_cast<const float*>(a.x),
+                                                    static_cast<const float*>(a.w_router), a.logits_scratch);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
   if (a.S == 0) return cudaSuccess;
   SelectParams sp{a.E,        a.K,      a.score_fn, a.renormalize, a.num_groups,   a.topk_groups, a.tau,
@@ -473,40 +509,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
     return cudaGetLastError();
   }
   if (logits == nullptr) {
-    cudaError_t err;
-    if (a.act_dtype == MOE_BF16 && a.d % 8 == 0) {
-      // l = x W_r^T as one dense GEMM on the tensor cores (fp32 accumulate
-      // and output); the selection then reads the logits back
-      GemmArgs g{};
-      g.epilogue = EPI_NONE;
-      g.groups = nullptr;
-      g.num_groups = 1;
-      g.shared_slab = -1;
-      g.a = a.x;
-      g.a_rows = a.S;
-      g.b0 = a.w_router;
-      g.b_rows = a.E;
-      g.n_per_slab = a.E;
-      g.N = a.E;
-      g.K = a.d;
-      g.out = a.logits_scratch;
-      g.out_rows = a.S;
-      g.out_f32 = 1;
-      g.max_total_rows = a.S;
-      g.max_group_rows = a.S;
-      g.status = a.status;
-      err = launch_grouped_gemm_tc(g, a.num_sms, stream);
-    } else {
-      dim3 grid((a.S + 31) / 32, (a.E + 63) / 64);
-      if (a.act_dtype == MOE_BF16)
-        logits_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a.S, a.d, a.E, static_cast<const __nv_bfloat16*>(a.x),
-                                                                static_cast<const __nv_bfloat16*>(a.w_router),
-                                                                a.logits_scratch);
-      else
-        logits_kernel<float><<<grid, 256, 0, stream>>>(a.S, a.d, a.E, static_cast<const float*>(a.x),
-                                                        static_cast<const float*>(a.w_router), a.logits_scratch);
-      err = cudaGetLastError();
-    }
+    const cudaError_t err = launch_router_logits(a, stream);
     if (err != cudaSuccess) return err;
     logits = a.logits_scratch;
   }
