@@ -193,7 +193,7 @@ typedef struct {
  * be given).  The product is taken as scale * B (A x): the projection's own
  * product stays that of the shared weights, and the adapter's share is added
  * to its fp32 sum before the channel bias, the activation or the combine.
- *   num_adapters N >= 1; rank r: a multiple of 8, at most MOE_LORA_MAX_RANK
+ *   num_adapters N, 1 .. MOE_LORA_MAX_ADAPTERS; rank r: a multiple of 8, at most MOE_LORA_MAX_RANK
  *     (adapters of smaller ranks are padded with zeros).
  *   All pointers DEVICE, 16-byte aligned (scale 4-byte), row-major bf16:
  *     a_gate, a_up [N][E+ns][r][d], b_gate, b_up [N][E+ns][h][r],
@@ -207,6 +207,7 @@ typedef struct {
  * multiplied with the bf16 tokens and hidden rows).
  */
 #define MOE_LORA_MAX_RANK 128
+#define MOE_LORA_MAX_ADAPTERS 4096
 typedef struct {
   int32_t num_adapters;
   int32_t rank;
@@ -405,8 +406,8 @@ moe_status moe_layer_forward_timed(const moe_desc *desc, const moe_weights *w, c
 
 /*
  * The whole layer for a few tokens in ONE kernel: S <= MOE_DECODE_MAX_TOKENS.
- * Same arguments, weights and results (up to fp32 summation order) as
- * moe_layer_forward, plus optional adapters (lora and adapter_of_token, both
+ * Same arguments, weights and results as moe_layer_forward (up to fp32
+ * summation order; router logits and selection keys are fp64 here), plus optional adapters (lora and adapter_of_token, both
  * NULL or both given).  The expert outputs are summed in fp32 (no bf16
  * rounding per expert); the hidden rows are bf16 (two-term or W8A8 codes with
  * E4M3 weights), as in moe_grouped_ffn.  A capacity changes nothing (no row
@@ -434,8 +435,11 @@ moe_status moe_layer_decode(const moe_desc *desc, const moe_weights *w, const mo
  * tokens.  moe_grouped_ffn_lora: moe_grouped_ffn's arguments plus lora,
  * adapter_of_token [S] and token_of_row [R] (moe_permute's output; rows with
  * -1 are not computed).  moe_layer_forward_lora: moe_layer_forward's arguments
- * plus lora and adapter_of_token.  The adapters' inner products A x are summed
- * in fp32 and kept as bf16 between the two products.  ws: at least
+ * plus lora and adapter_of_token; it selects on fp64 logits and keys, as
+ * moe_layer_decode does (moe_route: fp32), so experts whose keys are closer than
+ * fp32 tells apart may be picked differently from the staged calls.  The
+ * adapters' inner products A x are summed in fp32 and kept as bf16 between the
+ * two products, their share of a sum is bf16.  ws: at least
  * moe_lora_workspace_size bytes, otherwise as moe_layer_forward.  reroute = 1
  * is supported by both as by the calls without adapters.
  */

@@ -276,32 +276,57 @@ moe_status permute_impl(const moe_desc& d, const void* x, const int32_t* topk_id
 }
 
 // Adapters of one call: the kernels' view, and the regions behind the layer's
-// own workspace that hold the inner products and the deltas.
+// own workspace that hold the tiles of rows, the inner products and the deltas.
 struct LoraCall {
   LoraParams p{};
   const int32_t* token_of_row = nullptr;
-  void* u = nullptr;
+  LoraPlan plan{};
+  float* u = nullptr;
   void* delta = nullptr;
+  float* logits = nullptr;  // layer call: the router's fp32 logits
 };
 
 struct LoraLayout {
-  size_t u, delta, total;
+  size_t counts, tiles, list, has, u, delta, logits, total;
 };
 
 LoraLayout lora_layout(const moe_desc& d, const moe_lora& l) {
-  const int64_t rows = routed_rows(d) + static_cast<int64_t>(d.num_shared) * d.num_tokens;
+  const int64_t S = d.num_tokens;
+  const int64_t rows = routed_rows(d) + d.num_shared * S, used = S * (d.top_k + d.num_shared);
   const int64_t pairs = d.activation == MOE_ACT_SWIGLU ? 2 : 1;
   const int64_t cols = pairs * d.d_ff > d.d_model ? pairs * d.d_ff : d.d_model;
   LoraLayout L;
-  L.u = make_layout(d).total;
-  L.delta = L.u + align_up(static_cast<size_t>(rows * pairs * l.rank) * 2);
-  L.total = L.delta + align_up(static_cast<size_t>(rows * cols) * 2);
+  size_t o = make_layout(d).total;
+  auto take = [&](int64_t bytes) {
+    const size_t at = o;
+    o = align_up(o + static_cast<size_t>(bytes));
+    return at;
+  };
+  L.counts = take(kAlign);
+  L.tiles = take(used * sizeof(LoraTile));
+  L.list = take(used * sizeof(int2));
+  L.has = take(rows);
+  L.u = take(kLoraMaxSplits * used * pairs * l.rank * 4);
+  L.delta = take(rows * cols * 2);
+  L.logits = take(d.num_experts > kRouteExactAll ? S * d.num_experts * 4 : 0);
+  L.total = o;
   return L;
+}
+
+void lora_regions(const LoraLayout& L, void* ws, LoraCall* c) {
+  char* base = static_cast<char*>(ws);
+  c->plan.counts = reinterpret_cast<int*>(base + L.counts);
+  c->plan.tiles = reinterpret_cast<LoraTile*>(base + L.tiles);
+  c->plan.list = reinterpret_cast<int2*>(base + L.list);
+  c->plan.has = reinterpret_cast<uint8_t*>(base + L.has);
+  c->u = reinterpret_cast<float*>(base + L.u);
+  c->delta = base + L.delta;
+  c->logits = reinterpret_cast<float*>(base + L.logits);
 }
 
 // Checks of a moe_lora against the layer (not of device data).
 moe_status lora_status(const moe_desc& d, const moe_lora* l) {
-  if (l == nullptr || l->num_adapters < 1) return MOE_ERR_INVALID_ARG;
+  if (l == nullptr || l->num_adapters < 1 || l->num_adapters > MOE_LORA_MAX_ADAPTERS) return MOE_ERR_INVALID_ARG;
   if (l->rank < 8 || l->rank % 8 != 0 || l->rank > MOE_LORA_MAX_RANK) return MOE_ERR_INVALID_ARG;
   if (d.act_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
@@ -484,30 +509,41 @@ moe_status ffn_impl(const moe_desc& d, const moe_weights& w, const void* x_perm,
       return cudaSuccess;
     LoraRowsArgs a{};
     a.lora = lora->p;
+    a.plan = lora->plan;
     a.m0 = m0;
     a.pairs = pairs;
-    a.groups = g.groups;
-    a.num_groups = g.num_groups;
     a.shared_slab = d.num_shared ? E : -1;
     a.slabs = slabs;
-    a.token_of_row = lora->token_of_row;
-    a.S = S;
     a.src = src;
     a.src_by_token = by_token;
     a.src_shared = src_shared;
-    a.rows = Rt;
     a.max_total_rows = g.max_total_rows;
     a.K = g.K;
     a.N = g.N;
     a.u = lora->u;
     a.delta = lora->delta;
-    a.status = status;
     a.num_sms = sms;
     g.delta = lora->delta;
+    g.delta_has = lora->plan.has;
     return launch_lora_rows(a, st);
   };
   if (terms && !a_quantized && (err = quant_up(up)) != cudaSuccess) return MOE_ERR_CUDA;
   const bool swiglu = d.activation == MOE_ACT_SWIGLU;
+  if (lora != nullptr) {
+    LoraPlanArgs a{};
+    a.lora = lora->p;
+    a.groups = g1;
+    a.num_groups = up.num_groups;
+    a.shared_slab = d.num_shared ? E : -1;
+    a.slabs = slabs;
+    a.token_of_row = lora->token_of_row;
+    a.S = S;
+    a.rows = Rt;
+    a.max_total_rows = up.max_total_rows;
+    a.plan = lora->plan;
+    a.status = status;
+    if (launch_lora_plan(a, st) != cudaSuccess) return MOE_ERR_CUDA;
+  }
   if ((err = adapt(up, swiglu ? 0 : 1, swiglu ? 2 : 1, a_quantized ? x : x_perm, a_quantized,
                    d.num_shared ? x : nullptr)) != cudaSuccess)
     return MOE_ERR_CUDA;
@@ -594,7 +630,14 @@ moe_status layer_impl(const moe_desc* desc, const moe_weights* w, const void* x,
   void* y_perm = at<void>(ws, L.y_perm);
   if (!record(events, 0, st)) return MOE_ERR_CUDA;
   const int terms = a_terms(d);
-  if ((s = route_impl(d, w, x, nullptr, idx, gates, ws, st)) != MOE_OK) return s;
+  if (lora != nullptr) {
+    RouteArgs a = route_args(d, w, x, nullptr, idx, gates, ws);
+    a.logits_scratch = lora->logits;
+    s = cuda_status(launch_route_exact(a, st));
+  } else {
+    s = route_impl(d, w, x, nullptr, idx, gates, ws, st);
+  }
+  if (s != MOE_OK) return s;
   if (d.reroute == 1) {
     // capacity ranks of the first choices, then the excess slots move; the
     // permutation below is that of the final choices
@@ -787,8 +830,7 @@ moe_status moe_grouped_ffn_lora(const moe_desc* desc, const moe_weights* w, cons
   LoraCall call;
   call.p = lora_params(*lora, adapter_of_token);
   call.token_of_row = token_of_row;
-  call.u = at<void>(ws, L.u);
-  call.delta = at<void>(ws, L.delta);
+  lora_regions(L, ws, &call);
   return ffn_impl(*desc, *w, x_perm, offsets, x, y_perm, ws, static_cast<cudaStream_t>(stream), false, false, nullptr,
                   &call);
 }
@@ -807,8 +849,7 @@ moe_status moe_layer_forward_lora(const moe_desc* desc, const moe_weights* w, co
   if ((s = lora_pointers(*desc, *lora, adapter_of_token)) != MOE_OK) return s;
   LoraCall call;
   call.p = lora_params(*lora, adapter_of_token);
-  call.u = at<void>(ws, L.u);
-  call.delta = at<void>(ws, L.delta);
+  lora_regions(L, ws, &call);
   return layer_impl(desc, w, x, y, topk_idx, topk_w, counts, ws, ws_bytes, stream, nullptr, &call);
 }
 

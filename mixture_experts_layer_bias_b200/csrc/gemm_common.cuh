@@ -42,6 +42,7 @@ struct TcParams {
   const float* row_scale;         // E4M3 activations: per-row scale of the A operand rows (nullptr: none)
   const float* row_scale_shared;  // ... of the shared expert's A rows (indexed by row within the group)
   const __nv_bfloat16* delta;     // adapters' share of the sums [out_rows][pcols] (LORA kernels)
+  const uint8_t* delta_has;       // rows that delta has
   StatusBlock* status;
 };
 
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(256) splitk_finalize_kernel(TcParams p) {
   float4 g, u;
   splitk_sums4<EPI == EPI_SWIGLU>(src, N, slice, ks, g, u);
   float dg[4] = {0.f, 0.f, 0.f, 0.f}, du[4] = {0.f, 0.f, 0.f, 0.f};
-  if (LORA) {
+  if (LORA && p.delta_has[orow]) {
     const __nv_bfloat16* dl = p.delta + orow * p.pcols + n;
     bf16x4_to_f32(*reinterpret_cast<const uint2*>(dl), dg);
     if (EPI == EPI_SWIGLU) bf16x4_to_f32(*reinterpret_cast<const uint2*>(dl + N), du);

@@ -71,6 +71,7 @@ cudaError_t launch_grouped_gemm_tc(const GemmArgs& a, int num_sms, cudaStream_t 
   p.row_scale = a.fp8 ? a.row_scale : nullptr;
   p.row_scale_shared = a.fp8 ? a.row_scale_shared : nullptr;
   p.delta = static_cast<const __nv_bfloat16*>(a.delta);
+  p.delta_has = a.delta_has;
   if (a.fp8 && a.row_scale == nullptr) return cudaErrorInvalidValue;
   return launch_grouped_gemm_single(a, p, num_sms, stream);
 }

@@ -173,6 +173,7 @@ __device__ __forceinline__ void epilogue_store(const TcParams& p, const TileInfo
   const bool full = p.tma_out && (row - lane) + 32 <= ti.grp.rows;  // warp-uniform
   const int64_t sbase = static_cast<int64_t>(ti.grp.expert) * N;
   const float rs = valid ? a_row_scale(p, ti.grp, row) : 1.0f;
+  const bool has = LORA && valid && p.delta_has[orow] != 0;
   constexpr int kChunks = (EPI == EPI_SWIGLU) ? 4 : 8;
   constexpr bool kBias = EPI == EPI_GELU_BIAS || EPI == EPI_BIAS;
   for (int c = half * (kChunks / 2); c < (half + 1) * (kChunks / 2); ++c) {
@@ -191,7 +192,7 @@ __device__ __forceinline__ void epilogue_store(const TcParams& p, const TileInfo
       const __nv_bfloat16* d0 = p.delta + orow * p.pcols + n;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bool in = valid && n + 8 * j + 8 <= N;
+        const bool in = has && n + 8 * j + 8 <= N;
         dl[j] = in ? ldg16(d0 + 8 * j) : make_uint4(0, 0, 0, 0);
         if (EPI == EPI_SWIGLU) dl1[j] = in ? ldg16(d0 + N + 8 * j) : make_uint4(0, 0, 0, 0);
       }

@@ -42,6 +42,10 @@ struct RouteArgs {
   float* score_out;         // optional [S][E]: gate sources (logits or sigmoid scores), with cand_key_out
 };
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
+// The same selection on fp64 keys (bf16 layers; logits computed).  Up to
+// kRouteExactAll experts need no logits_scratch [S][E].
+constexpr int kRouteExactAll = 32;
+cudaError_t launch_route_exact(const RouteArgs& a, cudaStream_t stream);
 // x W_r^T alone, into logits_scratch.
 cudaError_t launch_router_logits(const RouteArgs& a, cudaStream_t stream);
 
@@ -134,6 +138,7 @@ struct GemmArgs {
   const float* row_scale;        // [a rows] per-row scale of A (fp8 only)
   const float* row_scale_shared; // [S] per-row scale of the shared expert's A rows (fp8 only)
   const void* delta;        // adapters' share, bf16 [out_rows][N] (SwiGLU: [out_rows][2N], gate then up), or nullptr
+  const uint8_t* delta_has; // [out_rows]: 1 where delta has the row
   StatusBlock* status;
 };
 cudaError_t launch_grouped_gemm_tc(const GemmArgs& a, int num_sms, cudaStream_t stream);
@@ -191,29 +196,50 @@ struct LoraParams {
   const int32_t* ids;      // [S]: adapter of each token, -1 = none
 };
 
-// Inner products u = A row of every row of the groups, then the outer ones
-// delta = scale * B u, for `pairs` pairs from pair m0 (2: gate and up, N
-// columns each; 1: one).  Row i of a group is row r = out_row0 + i of the row
-// space; its token is token_of_row[r] (i for the shared expert's group) and
-// its input row: src row r, src row `token` (src_by_token), or, for the shared
-// expert's group, src_shared row i when given.  delta rows of tokens without
-// an adapter are zero.
-struct LoraRowsArgs {
+// The rows that have adapters, as tiles of up to kLoraTileRows rows of one
+// (expert, adapter): made once per call, used by every projection's products.
+constexpr int kLoraTileRows = 64;
+constexpr int kLoraMaxAdapters = MOE_LORA_MAX_ADAPTERS;
+constexpr int kLoraMaxSplits = 8;
+struct LoraTile {
+  int expert, adapter, pos, rows;  // entries pos .. pos + rows - 1 of the row list
+};
+struct LoraPlan {
+  int* counts;         // [2]: tiles, listed rows
+  LoraTile* tiles;     // [max_total_rows]
+  int2* list;          // [max_total_rows]: (row of the row space, token)
+  uint8_t* has;        // [rows]: 1 where the row's token has an adapter (rows of the groups only)
+};
+struct LoraPlanArgs {
   LoraParams lora;
-  int m0, pairs;
   const GroupEntry* groups;
   int num_groups, shared_slab, slabs;
   const int32_t* token_of_row;
   int S;
+  int64_t rows;            // rows of the row space
+  int64_t max_total_rows;  // bound of the rows of all groups together
+  LoraPlan plan;
+  StatusBlock* status;
+};
+cudaError_t launch_lora_plan(const LoraPlanArgs& a, cudaStream_t stream);
+
+// Inner products u = A row, then the outer ones delta = scale * B u, for
+// `pairs` pairs from pair m0 (2: gate and up, N columns each; 1: one), of the
+// planned rows.  Row r's input row: src row r, src row `token` (src_by_token),
+// or, for the shared expert's rows, src_shared row `token` when given.  delta
+// rows of tokens without an adapter are not written (see has).
+struct LoraRowsArgs {
+  LoraParams lora;
+  LoraPlan plan;
+  int m0, pairs;
+  int shared_slab, slabs;
   const void* src;
   int src_by_token;
   const void* src_shared;
-  int64_t rows;            // rows of the row space
-  int64_t max_total_rows;  // bound of the rows of all groups together
+  int64_t max_total_rows;
   int K, N;                // input and output width
-  void* u;                 // bf16 [rows][pairs][r]
+  float* u;                // fp32 [splits][max_total_rows][pairs * r]: the inner products, by slice of K
   void* delta;             // bf16 [rows][pairs * N]
-  StatusBlock* status;
   int num_sms;
 };
 cudaError_t launch_lora_rows(const LoraRowsArgs& a, cudaStream_t stream);

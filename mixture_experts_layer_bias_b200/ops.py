@@ -20,7 +20,7 @@ _lib = None
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE_STATUS = range(6)
 MOE_STATUS_NONFINITE_LOGIT, MOE_STATUS_BAD_EXPERT_ID, MOE_STATUS_TIMEOUT, MOE_STATUS_BAD_GROUP = 1, 2, 4, 8
 MOE_STATUS_DEBUG_CHECK, MOE_STATUS_BAD_ADAPTER = 0x10, 0x20
-MOE_DECODE_MAX_TOKENS, MOE_LORA_MAX_RANK = 64, 128
+MOE_DECODE_MAX_TOKENS, MOE_LORA_MAX_RANK, MOE_LORA_MAX_ADAPTERS = 64, 128, 4096
 MOE_NUM_COUNTERS = 8
 COUNTER_NAMES = ("nonfinite", "bad_id", "timeout", "overflow_rows", "rerouted")
 

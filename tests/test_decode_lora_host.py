@@ -98,7 +98,7 @@ def test_decode_refusals():
     assert _decode(_desc(num_tokens=0), None, None, None, x=None, y=None) == ops.MOE_OK
 
 
-BAD_LORA = [dict(num_adapters=0), dict(num_adapters=-1), dict(rank=0), dict(rank=12), dict(rank=136), dict(rank=-8)]
+BAD_LORA = [dict(num_adapters=0), dict(num_adapters=4097), dict(num_adapters=-1), dict(rank=0), dict(rank=12), dict(rank=136), dict(rank=-8)]
 BAD_POINTERS = [dict(b_gate=None), dict(a_up=None), dict(scale=None), dict(scale=0x30002), dict(a_down=0x30008),
                 dict(a_gate=None, b_gate=None, a_up=None, b_up=None, a_down=None, b_down=None)]
 
