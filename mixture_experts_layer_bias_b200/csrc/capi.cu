@@ -304,7 +304,7 @@ LoraLayout lora_layout(const moe_desc& d, const moe_lora& l) {
   };
   L.counts = take(kAlign);
   L.tiles = take(used * sizeof(LoraTile));
-  L.list = take(used * sizeof(int2));
+  L.list = take(kLoraTileRows * used * sizeof(int2));
   L.has = take(rows);
   L.u = take(kLoraMaxSplits * used * pairs * l.rank * 4);
   L.delta = take(rows * cols * 2);

@@ -95,6 +95,32 @@ __device__ __forceinline__ uint4 pack16<__nv_bfloat16>(const float* in) {
 __device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ void stg16(void* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
 
+// Read-only loads that stay where the program has them (volatile asm), so that
+// several are in flight before the first one's value is used; zero, without an
+// access, where !in.
+__device__ __forceinline__ uint4 ldg16_if(const void* p, bool in) {
+  uint4 r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+      : "l"(p), "r"(static_cast<int>(in)));
+  return r;
+}
+__device__ __forceinline__ uint2 ldg8_if(const void* p, bool in) {
+  uint2 r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+      "@p ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+      : "=&r"(r.x), "=&r"(r.y)
+      : "l"(p), "r"(static_cast<int>(in)));
+  return r;
+}
+
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 31; }
 
 // ----------------------------------------------------------------------------

@@ -198,16 +198,16 @@ struct LoraParams {
 
 // The rows that have adapters, as tiles of up to kLoraTileRows rows of one
 // (expert, adapter): made once per call, used by every projection's products.
-constexpr int kLoraTileRows = 64;
+constexpr int kLoraTileRows = 32;
 constexpr int kLoraMaxAdapters = MOE_LORA_MAX_ADAPTERS;
 constexpr int kLoraMaxSplits = 8;
 struct LoraTile {
-  int expert, adapter, pos, rows;  // entries pos .. pos + rows - 1 of the row list
+  int expert, adapter, pos, rows;  // its inner products: rows pos .. pos + rows - 1 of u
 };
 struct LoraPlan {
   int* counts;         // [2]: tiles, listed rows
   LoraTile* tiles;     // [max_total_rows]
-  int2* list;          // [max_total_rows]: (row of the row space, token)
+  int2* list;          // [32 max_total_rows]: tile i's rows from 32 i on: (row of the row space, token)
   uint8_t* has;        // [rows]: 1 where the row's token has an adapter (rows of the groups only)
 };
 struct LoraPlanArgs {

@@ -4,7 +4,7 @@
 //   delta = scale[a] B[a][e] u     added to the projection's fp32 sums by the
 //                                  grouped GEMM's epilogue
 // Requests share the experts, not the adapters, so the rows are first sorted by
-// (expert, adapter) into tiles of up to 64 rows that share one pair of adapter
+// (expert, adapter) into tiles of up to 32 rows that share one pair of adapter
 // matrices (lora_plan_kernel, once per call).  A tile's products then run on
 // m16n8k16 tensor-core instructions: both are bound by memory (the rows are
 // read once, the deltas written once, and an adapter's matrices are read once
@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
+#include "pdl.cuh"
 
 namespace moe {
 
@@ -65,6 +66,8 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const LoraPlanA
   __shared__ int hist[kLoraMaxAdapters];  // rows of each adapter, then its next entry
   __shared__ int warp_sums[kPlanThreads / 32];
   __shared__ int base_tile, base_row;
+  pdl_wait();
+  pdl_trigger();
   const GroupEntry ge = a.groups[blockIdx.x];
   const bool ok = ge.rows > 0 && ge.rows <= a.S && ge.expert >= 0 && ge.expert < a.slabs && ge.out_row0 >= 0 &&
                   static_cast<int64_t>(ge.out_row0) + ge.rows <= a.rows;
@@ -107,8 +110,8 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const LoraPlanA
   tile += base_tile;
   for (int i = a0; i < a1; ++i) {
     const int c = hist[i];
+    hist[i] = tile * kRows;  // the adapter's next entry
     for (int k = 0; k < c; k += kRows) a.plan.tiles[tile++] = LoraTile{ge.expert, i, row + k, min(kRows, c - k)};
-    hist[i] = row;
     row += c;
   }
   __syncthreads();
@@ -119,36 +122,59 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const LoraPlanA
   }
 }
 
+// A tile and its rows in shared memory, loaded one unit ahead: the entries of
+// tile i are list[32 i ..], so tile and rows load side by side.
+struct TileRows {
+  LoraTile tile;
+  int2 row[kRows];
+};
+struct MetaRegs {
+  LoraTile tile;
+  int2 row;
+};
+__device__ __forceinline__ MetaRegs meta_load(const LoraPlan& p, int tile) {
+  MetaRegs m{};
+  if (threadIdx.x < kRows) m.row = p.list[tile * kRows + threadIdx.x];  // (entries past the tile's rows: not used)
+  if (threadIdx.x == 0) m.tile = p.tiles[tile];
+  return m;
+}
+__device__ __forceinline__ void meta_store(TileRows& t, const MetaRegs& m) {
+  if (threadIdx.x < kRows) t.row[threadIdx.x] = m.row;
+  if (threadIdx.x == 0) t.tile = m.tile;
+}
+
 // Inner products of one (tile, slice of K) per unit.  N = pairs * r columns in
 // blocks of 32; warp w takes block w % nb and, of the slice, every kslices-th
-// piece of 32 k; the warps of a block add up in a fixed order through shared
-// memory.
+// piece of 32 k, the next piece's loads under way during a piece's products; the
+// warps of a block add up in a fixed order through shared memory.
 struct InnerShape {
   int splits;  // slices of K
   int chunk;   // k of a slice (a multiple of 32)
 };
 
-__global__ void __launch_bounds__(kThreads, 1) lora_inner_kernel(const LoraRowsArgs a, const InnerShape sh) {
-  __shared__ float red[kWarps][32][33];  // half of the rows at a time
-  __shared__ const __nv_bfloat16* rowp[kRows];
+__global__ void __launch_bounds__(kThreads, 2) lora_inner_kernel(const LoraRowsArgs a, const InnerShape sh) {
+  __shared__ float red[kWarps][kRows][33];
+  __shared__ TileRows meta[2];
   const int lane = lane_id(), warp = threadIdx.x >> 5, r = a.lora.r, q = lane & 3, gq = lane >> 2;
   const int cols = a.pairs * r, nb = (cols + 31) / 32, kslices = kWarps / nb;
   const int block = warp % nb, kslice = warp / nb;
+  pdl_wait();
+  pdl_trigger();
   const int units = a.plan.counts[0] * sh.splits;
-  for (int un = blockIdx.x; un < units; un += gridDim.x) {
-    const LoraTile tile = a.plan.tiles[un / sh.splits];
+  if (blockIdx.x < units) meta_store(meta[0], meta_load(a.plan, blockIdx.x / sh.splits));
+  __syncthreads();
+  for (int un = blockIdx.x, buf = 0; un < units; un += gridDim.x, buf ^= 1) {
+    const LoraTile tile = meta[buf].tile;
     const int split = un % sh.splits, k0 = split * sh.chunk, k1 = min(a.K, k0 + sh.chunk);
-    __syncthreads();
-    if (threadIdx.x < kRows) {
-      const int2 e = a.plan.list[tile.pos + min(static_cast<int>(threadIdx.x), tile.rows - 1)];
-      const __nv_bfloat16* p;
+    const int next = un + gridDim.x;
+    MetaRegs ahead{};
+    if (next < units) ahead = meta_load(a.plan, next / sh.splits);
+    auto row_of = [&](int i) {
+      const int2 e = meta[buf].row[min(i, tile.rows - 1)];
       if (tile.expert == a.shared_slab && a.src_shared != nullptr)
-        p = static_cast<const __nv_bfloat16*>(a.src_shared) + static_cast<int64_t>(e.y) * a.K;
-      else
-        p = static_cast<const __nv_bfloat16*>(a.src) + static_cast<int64_t>(a.src_by_token ? e.y : e.x) * a.K;
-      rowp[threadIdx.x] = p;
-    }
-    __syncthreads();
+        return static_cast<const __nv_bfloat16*>(a.src_shared) + static_cast<int64_t>(e.y) * a.K;
+      return static_cast<const __nv_bfloat16*>(a.src) + static_cast<int64_t>(a.src_by_token ? e.y : e.x) * a.K;
+    };
     // rows of A for this lane's column of each 8-column tile of the block (nullptr: no such column or no pair)
     const __nv_bfloat16* bp[4];
 #pragma unroll
@@ -159,128 +185,158 @@ __global__ void __launch_bounds__(kThreads, 1) lora_inner_kernel(const LoraRowsA
         bp[j] = static_cast<const __nv_bfloat16*>(a.lora.a[a.m0 + m]) +
                 ((static_cast<int64_t>(tile.adapter) * a.slabs + tile.expert) * r + (col - m * r)) * a.K;
     }
-    const int mt = (tile.rows + 15) / 16;
-    float acc[4][4][4];
+    const bool two = tile.rows > 16;
+    const __nv_bfloat16* ap[2][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i) {
+      ap[i][0] = row_of(i * 16 + gq);
+      ap[i][1] = row_of(i * 16 + gq + 8);
+    }
+    float acc[2][4][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.0f;
-    if (kslice < kslices) {
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      for (int k = k0 + kslice * 32; k < k1; k += kslices * 32) {
-        const int c = k + 8 * q;  // this lane's 8 k (K is a multiple of 8)
-        const bool in = c < k1;
-        uint4 av[4][2], bv[4];
+    struct Piece {
+      uint4 a[2][2], b[4];
+    };
+    auto load = [&](Piece& pc, int k) {
+      const int c = k + 8 * q;  // this lane's 8 k (K is a multiple of 8)
+      const bool in = c < k1;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bv[j] = in && bp[j] != nullptr ? ldg16(bp[j] + c) : zero;
+      for (int j = 0; j < 4; ++j) pc.b[j] = ldg16_if(bp[j] + c, in && bp[j] != nullptr);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          av[i][0] = in && i < mt ? ldg16(rowp[i * 16 + gq] + c) : zero;
-          av[i][1] = in && i < mt ? ldg16(rowp[i * 16 + gq + 8] + c) : zero;
-        }
+      for (int i = 0; i < 2; ++i) {
+        pc.a[i][0] = ldg16_if(ap[i][0] + c, in && (i == 0 || two));
+        pc.a[i][1] = ldg16_if(ap[i][1] + c, in && (i == 0 || two));
+      }
+    };
+    auto products = [&](const Piece& pc) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i < mt) {
+      for (int i = 0; i < 2; ++i) {
+        if (i == 0 || two) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mma_bf16(acc[i][j], av[i][0].x, av[i][1].x, av[i][0].y, av[i][1].y, bv[j].x, bv[j].y);
-              mma_bf16(acc[i][j], av[i][0].z, av[i][1].z, av[i][0].w, av[i][1].w, bv[j].z, bv[j].w);
-            }
+          for (int j = 0; j < 4; ++j) {
+            mma_bf16(acc[i][j], pc.a[i][0].x, pc.a[i][1].x, pc.a[i][0].y, pc.a[i][1].y, pc.b[j].x, pc.b[j].y);
+            mma_bf16(acc[i][j], pc.a[i][0].z, pc.a[i][1].z, pc.a[i][0].w, pc.a[i][1].w, pc.b[j].z, pc.b[j].w);
           }
         }
+      }
+    };
+    if (kslice < kslices) {
+      const int step = kslices * 32;
+      Piece p0, p1;
+      int k = k0 + kslice * 32;
+      if (k < k1) load(p0, k);
+      for (; k < k1; k += 2 * step) {
+        load(p1, k + step);  // past the slice: zeros
+        products(p0);
+        load(p0, k + 2 * step);
+        products(p1);
       }
     }
     // accumulator (i, j): rows 16 i + gq (+ 8), columns 8 j + 2 q (+ 1) of the block
     float* u = a.u + (static_cast<int64_t>(split) * a.max_total_rows + tile.pos) * cols;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (32 * h < tile.rows) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              red[warp][i * 16 + gq + (v >> 1) * 8][j * 8 + 2 * q + (v & 1)] = acc[2 * h + i][j][v];
-        __syncthreads();
-        for (int i = threadIdx.x; i < min(32, tile.rows - 32 * h) * cols; i += kThreads) {
-          const int row = i / cols, col = i - row * cols, b = col / 32;
-          float s = 0.0f;
-          for (int k = 0; k < kslices; ++k) s += red[k * nb + b][row][col - b * 32];
-          u[static_cast<int64_t>(32 * h + row) * cols + col] = s;
-        }
-        __syncthreads();
-      }
+        for (int v = 0; v < 4; ++v) red[warp][i * 16 + gq + (v >> 1) * 8][j * 8 + 2 * q + (v & 1)] = acc[i][j][v];
+    if (next < units) meta_store(meta[buf ^ 1], ahead);
+    __syncthreads();
+    for (int i = threadIdx.x; i < tile.rows * cols; i += kThreads) {
+      const int row = i / cols, col = i - row * cols, b = col / 32;
+      float s = 0.0f;
+      for (int k = 0; k < kslices; ++k) s += red[k * nb + b][row][col - b * 32];
+      u[static_cast<int64_t>(row) * cols + col] = s;
     }
+    __syncthreads();
   }
 }
 
-// Outer products of one (tile, kOuterCols columns of one pair) per unit.  The
+// Outer products of one (tile, kOuterCols columns of every pair) per unit.  The
 // tile's u (the slices' sums, rounded to bf16) sits in shared memory; warp w
-// makes 32 columns at a time.  Its column c of the 8-column tile j stands for
-// column 8 (c / 2) + 2 j + c % 2 of the 32, so that a lane ends with 8
-// neighbouring columns of its rows: one 16-byte store each.
+// makes 32 columns of a pair at a time, the next columns' rows of B under way
+// during the products.  Its column c of the 8-column tile j stands for column 8
+// (c / 2) + 2 j + c % 2 of the 32, so that a lane ends with 8 neighbouring
+// columns of its rows: one 16-byte store each.
 constexpr int kOuterCols = 2048;
 
-__global__ void __launch_bounds__(kThreads) lora_outer_kernel(const LoraRowsArgs a, int splits) {
-  __shared__ __align__(16) __nv_bfloat16 us[kRows][MOE_LORA_MAX_RANK + 8];
-  __shared__ int64_t out_row[kRows];
+template <int KSTEPS>  // 16-k steps of the rank kept in registers: r <= 16 KSTEPS
+__global__ void __launch_bounds__(kThreads, KSTEPS <= 2 ? 3 : 2) lora_outer_kernel(const LoraRowsArgs a, int splits) {
+  __shared__ __align__(16) __nv_bfloat16 us[2][kRows][16 * KSTEPS + 8];
+  __shared__ TileRows meta[2];
   const int lane = lane_id(), warp = threadIdx.x >> 5, r = a.lora.r, q = lane & 3, gq = lane >> 2;
-  const int cols = a.pairs * r, rp = (r + 15) & ~15;
+  const int cols = a.pairs * r, rp = 16 * KSTEPS;
   const int blocks = (a.N + kOuterCols - 1) / kOuterCols;
-  const int units = a.plan.counts[0] * a.pairs * blocks;
-  for (int un = blockIdx.x; un < units; un += gridDim.x) {
-    const LoraTile tile = a.plan.tiles[un / (a.pairs * blocks)];
-    const int m = un / blocks % a.pairs, n0 = un % blocks * kOuterCols;
-    __syncthreads();
-    if (threadIdx.x < kRows)
-      out_row[threadIdx.x] = a.plan.list[tile.pos + min(static_cast<int>(threadIdx.x), tile.rows - 1)].x;
-    for (int i = threadIdx.x; i < kRows * rp; i += kThreads) {
-      const int row = i / rp, c = i - row * rp;
+  pdl_wait();
+  pdl_trigger();
+  const int units = a.plan.counts[0] * blocks;
+  if (blockIdx.x < units) meta_store(meta[0], meta_load(a.plan, blockIdx.x / blocks));
+  __syncthreads();
+  for (int un = blockIdx.x, buf = 0; un < units; un += gridDim.x, buf ^= 1) {
+    const LoraTile tile = meta[buf].tile;
+    const int n0 = un % blocks * kOuterCols, nc = min(a.N - n0, kOuterCols);
+    const int next = un + gridDim.x;
+    MetaRegs ahead{};
+    if (next < units) ahead = meta_load(a.plan, next / blocks);
+    // rows of B of 32 columns: item `it` of the unit is column group it / pairs of pair it % pairs
+    const int items = (nc + 31) / 32 * a.pairs;
+    uint2 bv[KSTEPS][4];
+    auto load_b = [&](int it) {
+      const int m = it % a.pairs, n = n0 + it / a.pairs * 32;
+      const auto* b = static_cast<const __nv_bfloat16*>(a.lora.b[a.m0 + m]);
+      const bool any = it < items && b != nullptr;
+      if (any) b += (static_cast<int64_t>(tile.adapter) * a.slabs + tile.expert) * a.N * r;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = n + 8 * (gq >> 1) + 2 * j + (gq & 1);
+#pragma unroll
+        for (int k = 0; k < KSTEPS; ++k)
+          bv[k][j] = ldg8_if(b + static_cast<int64_t>(col) * r + 16 * k + 4 * q, any && col < a.N && 16 * k + 4 * q < r);
+      }
+    };
+    load_b(warp);
+    for (int i = threadIdx.x; i < a.pairs * kRows * rp; i += kThreads) {
+      const int m = i / (kRows * rp), row = i / rp % kRows, c = i % rp;
       float s = 0.0f;
       if (row < tile.rows && c < r && a.lora.a[a.m0 + m] != nullptr) {
         const float* src = a.u + static_cast<int64_t>(tile.pos + row) * cols + m * r + c;
         for (int k = 0; k < splits; ++k) s += __ldg(src + static_cast<int64_t>(k) * a.max_total_rows * cols);
       }
-      us[row][c] = __float2bfloat16_rn(s);
+      us[m][row][c] = __float2bfloat16_rn(s);
     }
     __syncthreads();
     const float scale = __ldg(a.lora.scale + tile.adapter);
-    const auto* b = static_cast<const __nv_bfloat16*>(a.lora.b[a.m0 + m]);
-    if (b != nullptr) b += (static_cast<int64_t>(tile.adapter) * a.slabs + tile.expert) * a.N * r;
-    const int mt = (tile.rows + 15) / 16;
-    for (int n = n0 + warp * 32; n < min(a.N, n0 + kOuterCols); n += kWarps * 32) {
-      float acc[4][4][4];
+    const bool two = tile.rows > 16;
+    for (int it = warp; it < items; it += kWarps) {
+      const int m = it % a.pairs, n = n0 + it / a.pairs * 32;
+      float acc[2][4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.0f;
-      for (int k = 0; k < rp; k += 16) {
-        uint2 bv[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int col = n + 8 * (gq >> 1) + 2 * j + (gq & 1);
-          bv[j] = b != nullptr && col < a.N && k + 4 * q < r
-                      ? __ldg(reinterpret_cast<const uint2*>(b + static_cast<int64_t>(col) * r + k + 4 * q))
-                      : make_uint2(0, 0);
-        }
+      for (int k = 0; k < KSTEPS; ++k) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i < mt) {
-            const uint2 u0 = *reinterpret_cast<const uint2*>(&us[i * 16 + gq][k + 4 * q]);
-            const uint2 u1 = *reinterpret_cast<const uint2*>(&us[i * 16 + gq + 8][k + 4 * q]);
+        for (int i = 0; i < 2; ++i) {
+          if (i == 0 || two) {
+            const uint2 u0 = *reinterpret_cast<const uint2*>(&us[m][i * 16 + gq][16 * k + 4 * q]);
+            const uint2 u1 = *reinterpret_cast<const uint2*>(&us[m][i * 16 + gq + 8][16 * k + 4 * q]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_bf16(acc[i][j], u0.x, u1.x, u0.y, u1.y, bv[j].x, bv[j].y);
+            for (int j = 0; j < 4; ++j) mma_bf16(acc[i][j], u0.x, u1.x, u0.y, u1.y, bv[k][j].x, bv[k][j].y);
           }
         }
       }
+      load_b(it + kWarps);
       const int col = n + 8 * q;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int hi = 0; hi < 2; ++hi) {
           const int row = i * 16 + gq + hi * 8;
@@ -288,13 +344,23 @@ __global__ void __launch_bounds__(kThreads) lora_outer_kernel(const LoraRowsArgs
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(acc[i][j][2 * hi] * scale, acc[i][j][2 * hi + 1] * scale);
-            stg16(static_cast<__nv_bfloat16*>(a.delta) + (out_row[row] * a.pairs + m) * a.N + col,
-                  make_uint4(w[0], w[1], w[2], w[3]));
+            const int64_t at = static_cast<int64_t>(meta[buf].row[row].x) * a.pairs + m;
+            stg16(static_cast<__nv_bfloat16*>(a.delta) + at * a.N + col, make_uint4(w[0], w[1], w[2], w[3]));
           }
         }
       }
     }
+    if (next < units) meta_store(meta[buf ^ 1], ahead);
+    __syncthreads();
   }
+}
+
+template <int KSTEPS>
+cudaError_t launch_outer(const LoraRowsArgs& a, int splits, cudaStream_t stream) {
+  const int64_t units = a.max_total_rows * ((a.N + kOuterCols - 1) / kOuterCols);
+  const int64_t cap = static_cast<int64_t>(KSTEPS <= 2 ? 3 : 2) * a.num_sms;
+  return launch_pdl(lora_outer_kernel<KSTEPS>, dim3(static_cast<unsigned>(units < cap ? units : cap)), dim3(kThreads), 0,
+                    stream, a, splits);
 }
 
 }  // namespace
@@ -303,7 +369,7 @@ cudaError_t launch_lora_plan(const LoraPlanArgs& a, cudaStream_t stream) {
   if (a.num_groups <= 0 || a.num_groups > gemm::kMaxGroups || a.lora.n > kLoraMaxAdapters) return cudaErrorInvalidValue;
   cudaError_t e = cudaMemsetAsync(a.plan.counts, 0, 2 * sizeof(int), stream);
   if (e != cudaSuccess) return e;
-  lora_plan_kernel<<<a.num_groups, kPlanThreads, 0, stream>>>(a);
+  lora_plan_kernel<<<a.num_groups, kPlanThreads, 0, stream>>>(a);  // (behind a memset: no dependent launch)
   return cudaGetLastError();
 }
 
@@ -317,14 +383,19 @@ cudaError_t launch_lora_rows(const LoraRowsArgs& a, cudaStream_t stream) {
   const int chunk = ((a.K + splits - 1) / splits + 31) & ~31;
   splits = (a.K + chunk - 1) / chunk;
   // the tile count is known on the device only: at most one per row
-  const int64_t inner = a.max_total_rows * splits, outer = a.max_total_rows * a.pairs * ((a.N + kOuterCols - 1) / kOuterCols);
-  lora_inner_kernel<<<static_cast<unsigned>(inner < a.num_sms * 2 ? inner : a.num_sms * 2), kThreads, 0, stream>>>(
-      a, InnerShape{splits, chunk});
-  cudaError_t e = cudaGetLastError();
+  const int64_t inner = a.max_total_rows * splits, cap = 2 * a.num_sms;
+  cudaError_t e = launch_pdl(lora_inner_kernel, dim3(static_cast<unsigned>(inner < cap ? inner : cap)), dim3(kThreads), 0,
+                             stream, a, InnerShape{splits, chunk});
   if (e != cudaSuccess) return e;
-  lora_outer_kernel<<<static_cast<unsigned>(outer < a.num_sms * 4 ? outer : a.num_sms * 4), kThreads, 0, stream>>>(
-      a, splits);
-  return cudaGetLastError();
+  if (a.lora.r <= 16)
+    e = launch_outer<1>(a, splits, stream);
+  else if (a.lora.r <= 32)
+    e = launch_outer<2>(a, splits, stream);
+  else if (a.lora.r <= 64)
+    e = launch_outer<4>(a, splits, stream);
+  else
+    e = launch_outer<8>(a, splits, stream);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace moe

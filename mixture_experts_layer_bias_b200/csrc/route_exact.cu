@@ -1,14 +1,16 @@
 // Router selection on fp64 keys for any number of tokens, a warp per token.
 //
-// A product of two bf16 numbers is exact in fp32, so the sum of the products in
-// fp64 gives each logit to about 2^-52 of its terms: two experts change places
-// only where the exact keys do.  Up to 32 experts, every logit is summed that
-// way (the conversion of each product to fp64, 16 lanes a clock and SM, is what
-// bounds it).  Above, the fp32 logits of the tensor-core GEMM select the K + 1
-// best experts first; those, and every expert that the GEMM's error bound leaves
-// within reach of the last of them, get exact logits, and the selection and the
-// gates are made from the exact ones only: K + 1 dot products a token instead of
-// E.
+// A product of two bf16 numbers is exact in fp64, so their fp64 sum gives each
+// logit to about 2^-52 of its terms: two experts change places only where the
+// exact keys do.  Up to 32 experts, every logit is summed that way, a CTA per 4
+// tokens: its four warps split d and take 4 tokens x 4 experts at a time, 16
+// fp64 multiply-adds for 4 conversions of tokens and 4 of weights, these by
+// integer operations (the conversion instruction, 16 a clock and SM, would bound
+// a dot product on its own).  Above, the fp32 logits of the tensor-core
+// GEMM select the K + 1 best experts first; those, and every expert that the
+// GEMM's error bound leaves within reach of the last of them, get exact logits,
+// and the selection and the gates are made from the exact ones only: K + 1 dot
+// products a token instead of E.
 //
 // Scores, selection bias, group limit and gates as in the routing kernels
 // (jsqmd.com "第11章 MoE模型推理" 11.1.1, 11.3.3; ybb.press "MoE 推理工程深层实战"
@@ -17,20 +19,21 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pdl.cuh"
 
 namespace moe {
 
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;  // and tokens of a CTA
 
 struct ExactParams {
   int S, d, E, K, score_fn, renormalize, num_groups, topk_groups;
   float tau;
   const __nv_bfloat16* x;
   const __nv_bfloat16* w;
-  const float* approx;  // [S][E] fp32 logits without the bias, or nullptr: every logit is summed in fp64
+  const float* approx;  // E > 32: [S][E] fp32 logits without the bias
   const float* router_bias;
   const float* sel_bias;
   int32_t* topk_idx;
@@ -67,41 +70,67 @@ __device__ __forceinline__ void warp_best(double& v, int& idx) {
   }
 }
 
-// Exact logits of n <= 4 experts e[]; with `norms` also the squared lengths of
-// their rows (fp32, a bound needs no more).
+// A bf16 (its bits in the upper half of `w`) as a double times 2^-896, by
+// moving its fields: exact for every finite value, subnormals included; an
+// infinity or a NaN becomes one.
+__device__ __forceinline__ double bf16_bits_to_f64(uint32_t w) {
+  uint32_t hi = (w >> 3) & 0x0FFFE000u;  // exponent and mantissa at the bottom of a double's exponent field
+  if (hi >= 0x0FF00000u) hi |= 0x7FF00000u;
+  return __hiloint2double(static_cast<int>(hi | (w & 0x80000000u)), 0);
+}
+constexpr double kUnscale = 0x1p896;
+
+// The q-th of 8 bf16 values, as the bits of a float.
+__device__ __forceinline__ uint32_t bf16_at(const uint4& v, int q) {
+  const uint32_t w = q < 2 ? v.x : q < 4 ? v.y : q < 6 ? v.z : v.w;
+  return (q & 1) ? (w & 0xFFFF0000u) : (w << 16);
+}
+
+// Exact logits of n <= 4 experts e[]; with NORMS also the largest squared length
+// of their rows and that of the token (fp32: a bound needs no more).
+template <bool NORMS>
 __device__ __forceinline__ void exact_logits(const ExactParams& p, const __nv_bfloat16* xr, const int (&e)[4], int n,
-                                             double (&out)[4], float* wnorm) {
+                                             double (&out)[4], float* wnorm, float* xnorm) {
   const int lane = lane_id();
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
-  float sq[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int c = lane * 8; c < p.d; c += 256) {
-    const uint4 xv = ldg16(xr + c);
-    uint4 wv[4];
+  float sq[4] = {0.f, 0.f, 0.f, 0.f}, xq = 0.0f;
+  const __nv_bfloat16* wr[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) wv[i] = ldg16(p.w + static_cast<int64_t>(e[i]) * p.d + c);
-    float xf[8];
-    unpack16<__nv_bfloat16>(xv, xf);
+  for (int i = 0; i < 4; ++i) wr[i] = p.w + static_cast<int64_t>(e[i < n ? i : 0]) * p.d;
+  uint4 xv, wv[4], xn, wn[4];  // this step's pieces and the next one's
+  auto load = [&](int c, uint4& x, uint4 (&w)[4]) {
+    x = ldg16_if(xr + c, c < p.d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i < n) {
-        float wf[8];
-        unpack16<__nv_bfloat16>(wv[i], wf);
+    for (int i = 0; i < 4; ++i) w[i] = ldg16_if(wr[i] + c, c < p.d && i < n);
+  };
+  auto add = [&](const uint4& x, const uint4 (&w)[4]) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          acc[i] += static_cast<double>(__fmul_rn(xf[q], wf[q]));
-          sq[i] = fmaf(wf[q], wf[q], sq[i]);
-        }
+    for (int q = 0; q < 8; ++q) {
+      const float xf = __uint_as_float(bf16_at(x, q));
+      if (NORMS) xq = fmaf(xf, xf, xq);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float wf = __uint_as_float(bf16_at(w[i], q));
+        acc[i] += static_cast<double>(__fmul_rn(xf, wf));  // the product is exact in fp32
+        if (NORMS) sq[i] = fmaf(wf, wf, sq[i]);
       }
     }
+  };
+  load(lane * 8, xv, wv);
+  for (int c = lane * 8; c < p.d; c += 512) {
+    load(c + 256, xn, wn);
+    add(xv, wv);
+    load(c + 512, xv, wv);
+    add(xn, wn);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (i < n) {
       out[i] = warp_sum_d(acc[i]) + (p.router_bias != nullptr ? static_cast<double>(__ldg(p.router_bias + e[i])) : 0.0);
-      if (wnorm != nullptr) *wnorm = fmaxf(*wnorm, warp_sum_f(sq[i]));
+      if (NORMS) *wnorm = fmaxf(*wnorm, warp_sum_f(sq[i]));
     }
   }
+  if (NORMS) *xnorm = warp_sum_f(xq);
 }
 
 template <int NI>
@@ -191,10 +220,70 @@ __device__ void group_limit(const ExactParams& p, const double (&key)[NI], bool 
   for (int i = 0; i < NI; ++i) cand[i] = cand[i] && chosen[i];
 }
 
+// Logits of the CTA's 4 tokens against all experts (at most 32), into out[4][E].
+__device__ void all_logits(const ExactParams& p, int t0, double (*part)[16], double* out) {
+  const int warp = threadIdx.x >> 5, lane = lane_id();
+  const __nv_bfloat16* xr[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) xr[i] = p.x + static_cast<int64_t>(min(t0 + i, p.S - 1)) * p.d;
+  for (int e0 = 0; e0 < p.E; e0 += 4) {
+    const __nv_bfloat16* wr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wr[i] = p.w + static_cast<int64_t>(min(e0 + i, p.E - 1)) * p.d;
+    double acc[16];  // [token][expert]
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.0;
+    for (int c = (warp * 32 + lane) * 8; c < p.d; c += kWarps * 256) {
+      uint4 xv[4], wv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xv[i] = ldg16_if(xr[i] + c, true);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wv[i] = ldg16_if(wr[i] + c, true);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        double xd[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xd[i] = static_cast<double>(__uint_as_float(bf16_at(xv[i], q)));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const double wd = bf16_bits_to_f64(bf16_at(wv[j], q));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i * 4 + j] = fma(xd[i], wd, acc[i * 4 + j]);
+        }
+      }
+    }
+    // reduce-scatter over the warp: lanes i and i + 16 end with the warp's sum of value i
+#pragma unroll
+    for (int s = 8; s >= 1; s >>= 1) {
+      const bool upper = (lane & s) != 0;
+#pragma unroll
+      for (int i = 0; i < s; ++i) {
+        const double send = upper ? acc[i] : acc[i + s], keep = upper ? acc[i + s] : acc[i];
+        acc[i] = keep + __shfl_xor_sync(kFull, send, s);
+      }
+    }
+    acc[0] += __shfl_xor_sync(kFull, acc[0], 16);
+    if (lane < 16) part[warp][lane] = acc[0];
+    __syncthreads();
+    if (threadIdx.x < 16) {
+      const int e = e0 + (lane & 3);
+      if (e < p.E)
+        out[(lane >> 2) * p.E + e] = ((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane])) * kUnscale +
+                                     (p.router_bias != nullptr ? static_cast<double>(__ldg(p.router_bias + e)) : 0.0);
+    }
+    __syncthreads();
+  }
+}
+
 template <int NI>
-__global__ void __launch_bounds__(kWarps * 32) route_exact_kernel(const ExactParams p) {
+__global__ void __launch_bounds__(kWarps * 32, NI <= 2 ? 5 : 4) route_exact_kernel(const ExactParams p) {
+  __shared__ double part[kWarps][16];
+  __shared__ double direct[kWarps * kRouteExactAll];
   const int lane = lane_id();
   const int tok = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_trigger();
+  if (NI == 1) all_logits(p, blockIdx.x * kWarps, part, direct);
   if (tok >= p.S) return;
   const __nv_bfloat16* xr = p.x + static_cast<int64_t>(tok) * p.d;
   Token<NI> t;
@@ -204,7 +293,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_exact_kernel(const ExactPar
       const int n = min(4, p.E - e0);
       const int e[4] = {e0, e0 + 1, e0 + 2, e0 + 3};
       double v[4];
-      exact_logits(p, xr, e, n, v, nullptr);
+      exact_logits<false>(p, xr, e, n, v, nullptr, nullptr);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (i < n) put<NI>(t, e[i], v[i]);
@@ -219,8 +308,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_exact_kernel(const ExactPar
     valid[i] = 32 * i + lane < p.E;
     t.logit[i] = neg_inf();
   }
-  if (p.approx == nullptr) {
-    all_exact();
+  if (NI == 1) {
+    if (valid[0]) t.logit[0] = direct[(threadIdx.x >> 5) * p.E + lane];
+    t.exact = 1;
   } else {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -241,13 +331,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_exact_kernel(const ExactPar
       group_limit<NI>(p, key, cand, &gap);
       // exact logits of the K + 1 best by the GEMM's logits
       float xn = 0.0f, wn = 0.0f;
-      for (int c = lane * 8; c < p.d; c += 256) {
-        float xf[8];
-        unpack16<__nv_bfloat16>(ldg16(xr + c), xf);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) xn = fmaf(xf[q], xf[q], xn);
-      }
-      xn = warp_sum_f(xn);
       double last = neg_inf();
       int pend[4] = {0, 0, 0, 0}, np = 0;
       uint32_t taken = 0;
@@ -276,7 +359,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_exact_kernel(const ExactPar
         }
         if (np == 4 || ((k == p.K || !found) && np > 0)) {
           double v[4];
-          exact_logits(p, xr, pend, np, v, &wn);
+          if (k < 4)
+            exact_logits<true>(p, xr, pend, np, v, &wn, &xn);
+          else
+            exact_logits<false>(p, xr, pend, np, v, nullptr, nullptr);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (i < np) put<NI>(t, pend[i], v[i]);
@@ -285,7 +371,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_exact_kernel(const ExactPar
         if (!found) break;
       }
       // The GEMM adds d / 16 products of 16 terms, each addition off by at most 2^-23 of the sum's largest part, which
-      // is at most |x| |w|; the picked rows' lengths stand for all rows'.  Twice that, in the key's units.
+      // is at most |x| |w|; the first picks' row lengths stand for all rows'.  Twice that, in the key's units.
       const double slope = p.score_fn == MOE_SCORE_SIGMOID ? 0.25 : 1.0 / static_cast<double>(p.tau);
       const double tol = 2.0 * slope * (p.d / 16 + 16) * 0x1p-23 * sqrt(static_cast<double>(xn) * wn);
       if (gap <= 2.0 * tol * (p.E / p.num_groups)) {
@@ -300,7 +386,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_exact_kernel(const ExactPar
             near &= near - 1;
             const int e[4] = {32 * i + src, 0, 0, 0};
             double v[4];
-            exact_logits(p, xr, e, 1, v, nullptr);
+            exact_logits<false>(p, xr, e, 1, v, nullptr, nullptr);
             if (lane == src) {
               t.logit[i] = v[0];
               t.exact |= 1u << i;
@@ -406,8 +492,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_exact_kernel(const ExactPar
 
 template <int NI>
 cudaError_t launch_ni(const ExactParams& p, cudaStream_t stream) {
-  route_exact_kernel<NI><<<(p.S + kWarps - 1) / kWarps, kWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  const cudaError_t e =
+      launch_pdl(route_exact_kernel<NI>, dim3((p.S + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, stream, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
