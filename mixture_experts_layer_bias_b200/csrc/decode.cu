@@ -24,11 +24,11 @@
 // one token tile: gate and up rows of the same 128 hidden columns (SwiGLU), or
 // 256 neighbouring output columns.  All steps of a phase, in the order (group,
 // tile, k) for up and (tile, group, k) for down, are cut into one equal range
-// per CTA, so every SM reads the same bytes whatever the group sizes are.  An up
-// tile cut by a range border is joined through fp32 partial sums in the
-// workspace by whichever CTA arrives last; the down phase's sums all go through
-// such partial tiles and are added by the whole grid at the end.  Both add in
-// CTA order, so results do not depend on timing.
+// per CTA, so every SM reads the same bytes whatever the group sizes are.  A tile
+// cut by a range border goes through fp32 partial sums in the workspace: in the
+// up phase whichever of its CTAs arrives last joins them, in the down phase the
+// whole grid adds them at the end, together with the gate-weighted sum over a
+// token's experts.  Both add in CTA order, so results do not depend on timing.
 //
 // Token tile of the up phase: while all tokens fit into the 16 columns that an
 // MMA has at least, every group uses all of them, straight from x.  Otherwise
@@ -37,9 +37,10 @@
 // held the up phase at 4.8 TB/s for one token.)
 //
 // Roles (384 threads): warp 0 feeds a ring of stages by TMA, warp 1 issues the
-// MMAs, warps 4 - 11 are the epilogue, two per TMEM lane quarter.  The weights of the down phase do not
-// depend on the hidden rows, so the producer fills the whole ring with them
-// while the up phase drains and the grid waits for the last hidden row.
+// MMAs, warps 4 - 11 are the epilogue, two per TMEM lane quarter.  The weights of
+// the down phase do not depend on the hidden rows, so the producer fills the
+// whole ring with them while the up phase drains and the grid waits for the last
+// hidden row.
 //
 // E4M3 weights: the tokens' codes (one or two per element, see quant.cu) are
 // separate columns of the same product, added in the epilogue.  The codes of a
@@ -47,9 +48,11 @@
 // not matter) while the up phase stores the bf16 hidden rows, and the epilogue
 // warps write the codes between the phases.
 //
-// Adapters: the epilogue warps take the inner products u = A x while the
-// tensor cores start on the up phase (and A hidden at the start of the down
-// phase), and add scale * B u where a tile's sums are final.
+// Adapters: while the tensor cores start on a phase, the epilogue warps of the
+// whole grid take the inner products u = A x (up) or A hidden (down) and then the
+// outer ones scale * B u, in equal shares, into fp32 buffers; the epilogue adds
+// those to a tile's final sums.  (Made by the epilogue itself, tile by tile, the
+// outer products kept the CTAs of the busiest expert 150 us longer than the others.)
 //
 // Every wait is bounded: a CTA that gives up reports MOE_STATUS_TIMEOUT, lets
 // its copies and MMAs in flight finish, frees its TMEM and leaves; the others'
@@ -83,7 +86,7 @@ constexpr size_t kSmemLimit = 232448;  // 227 KB per CTA
 // Grid-wide arrival counters, in the workspace's first 256 bytes behind the
 // status block: they count up within one call; the last CTA to leave the
 // kernel sets them back to zero.
-enum Arrival { kRouted, kSelected, kPacked, kInnerUp, kHidden, kCoded, kSummed, kNumArrivals };
+enum Arrival { kRouted, kSelected, kPacked, kInnerUp, kOuterUp, kHidden, kCoded, kInnerDown, kOuterDown, kSummed, kNumArrivals };
 struct GridSync {
   uint32_t arrived[kNumArrivals];
   uint32_t left;
@@ -93,7 +96,7 @@ static_assert(sizeof(StatusBlock) <= kSyncOffset, "the arrival counters sit behi
 static_assert(kSyncOffset + sizeof(GridSync) <= 256, "the arrival counters sit in the initialised block");
 
 struct Ws {
-  size_t logits, idx, gate, xq, xs, xp, hidden, amax, hq, hs, u_in, u_out, joins, partial, total;
+  size_t logits, idx, gate, xq, xs, xp, hidden, amax, hq, hs, u_in, u_out, d_in, d_out, outs, joins, partial, total;
 };
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -122,6 +125,9 @@ Ws ws_layout(int S, int d, int E, int K, int h, int ns, int terms, int rank) {
   L.hs = take(terms ? rows * 4 : 0);
   L.u_in = take(rows * 2 * rank * 4);
   L.u_out = take(rows * rank * 4);
+  L.d_in = take(rank ? rows * 2 * h * 4 : 0);
+  L.d_out = take(rank ? rows * d * 4 : 0);
+  L.outs = take(rows * d * 4);
   // per CTA: a counter for the cut up tile that begins in it, and two tiles' partial sums
   L.joins = take(kDecodeMaxCtas * 4);
   L.partial = take(static_cast<size_t>(kDecodeMaxCtas) * 2 * S * 256 * 4);
@@ -141,8 +147,11 @@ struct Params {
   uint32_t* amax;
   uint8_t* hq;
   float* hs;
-  float* u_in;
+  float* u_in;   // adapters: inner products [row][2][r], [row][r]
   float* u_out;
+  float* d_in;   // outer products [row][2][h], [row][d]
+  float* d_out;
+  float* outs;   // expert outputs [row][d] (down tiles that lie in one CTA)
   uint32_t* joins;
   float* partial;
   StatusBlock* status;
@@ -166,6 +175,7 @@ struct Ctl {
   int warp_sums[kWarps];
   int first[kMaxSlabs + 1];            // active group -> its first row
   int row0[kMaxSlabs];                 // slab -> its first row
+  int group[kMaxSlabs];                // slab -> its active group
   int slab[kMaxSlabs];                 // active group -> weight slab
   uint64_t mask[kMaxSlabs];            // active group -> its tokens
   uint64_t tokens_of[kMaxSlabs];       // slab -> its tokens
@@ -184,15 +194,16 @@ struct Scratch {
 struct Tables {
   Ctl* c;
   Scratch* scratch;
-  float* y;            // [S][256]: the down phase's sums of one tile, column n owned by one thread
   float* row_gate;     // row -> its gate
   float* row_scale;    // E4M3: row -> its codes' scale (tokens, then hidden rows)
   uint16_t* row_tok;   // row -> its token
+  uint16_t* row_grp;   // row -> its active group
+  uint16_t* slot_row;  // [S][K]: slot -> its row
 };
 
 size_t tables_bytes(int S, int K, int ns) {
   const size_t rows = static_cast<size_t>(S) * (K + ns);
-  return ((sizeof(Ctl) + 15) & ~size_t(15)) + static_cast<size_t>(S) * 256 * 4 + ((rows * 10 + 15) & ~size_t(15));
+  return ((sizeof(Ctl) + 15) & ~size_t(15)) + ((rows * 12 + static_cast<size_t>(S) * K * 2 + 15) & ~size_t(15));
 }
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
@@ -286,28 +297,6 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
   return v;
-}
-
-// scale * sum_r u[r] B[a][slab][n][r], by one thread.
-__device__ float adapter_delta(const LoraParams& l, int m, int slabs, int a, int slab, int out, int n, const float* u) {
-  const auto* b = static_cast<const __nv_bfloat16*>(l.b[m]) +
-                  ((static_cast<int64_t>(a) * slabs + slab) * out + n) * l.r;
-  float acc = 0.0f;
-  for (int i = 0; i < l.r; i += 8) {
-    float bf[8];
-    coding::bf16x8_to_f32(ldg16(b + i), bf);
-    const float4 u0 = __ldcg(reinterpret_cast<const float4*>(u + i));
-    const float4 u1 = __ldcg(reinterpret_cast<const float4*>(u + i + 4));
-    acc = fmaf(bf[0], u0.x, acc);
-    acc = fmaf(bf[1], u0.y, acc);
-    acc = fmaf(bf[2], u0.z, acc);
-    acc = fmaf(bf[3], u0.w, acc);
-    acc = fmaf(bf[4], u1.x, acc);
-    acc = fmaf(bf[5], u1.y, acc);
-    acc = fmaf(bf[6], u1.z, acc);
-    acc = fmaf(bf[7], u1.w, acc);
-  }
-  return acc * __ldg(l.scale + a);
 }
 
 // Router logits, a CTA per (expert, 8 tokens), the threads striding over d in
@@ -542,7 +531,10 @@ __device__ bool tables_phase(const Params& p, const Tables& t) {
     c.slab[group] = tid;
     c.mask[group] = mask;
   }
-  if (tid < slabs) c.row0[tid] = row0;
+  if (tid < slabs) {
+    c.row0[tid] = row0;
+    c.group[tid] = group;
+  }
   if (tid == kThreads - 1) {
     const int all = before + v;
     c.active = all >> 16;
@@ -555,7 +547,9 @@ __device__ bool tables_phase(const Params& p, const Tables& t) {
     const int e = shared ? a.E : sc.idx[i];
     const int r = c.row0[e] + __popcll(c.tokens_of[e] & ((uint64_t(1) << tok) - 1));
     t.row_tok[r] = static_cast<uint16_t>(tok);
+    t.row_grp[r] = static_cast<uint16_t>(c.group[e]);
     t.row_gate[r] = shared ? 1.0f : sc.gate[i];
+    if (!shared) t.slot_row[i] = static_cast<uint16_t>(r);
     if (a.terms) t.row_scale[r] = __ldcg(p.xs + tok);
   }
   if (blockIdx.x == 0) {
@@ -588,21 +582,9 @@ __device__ bool tables_phase(const Params& p, const Tables& t) {
   return grid_barrier(p, c, kPacked);
 }
 
-__device__ __forceinline__ int group_of_row(const Ctl& c, int r) {
-  int lo = 0, hi = c.active;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (c.first[mid] <= r)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
-}
-
 // Epilogue warps: u[row][m][i] = A_m[a][slab][i] . row for the pairs m0 .. m0 +
 // nm - 1, a warp per (row, pair, 8 values): the row's pieces meet eight rows of
-// A, nine loads in flight per lane and step.
+// A, two steps of nine loads in flight per lane.
 __device__ void adapter_inner(const Params& p, const Tables& t, int m0, int nm) {
   const LoraParams& l = p.a.lora;
   const int rows = t.c->first[t.c->active], slabs = p.a.E + p.a.num_shared, blocks = l.r / 8;
@@ -612,7 +594,7 @@ __device__ void adapter_inner(const Params& p, const Tables& t, int m0, int nm) 
   for (int i = blockIdx.x + gridDim.x * warp; i < rows * nm * blocks; i += gridDim.x * (kEpiThreads / 32)) {
     const int j = i % blocks * 8, m = m0 + (i / blocks) % nm, r = i / (blocks * nm);
     if (l.a[m] == nullptr) continue;
-    const int slab = t.c->slab[group_of_row(*t.c, r)];
+    const int slab = t.c->slab[t.row_grp[r]];
     const int token = t.row_tok[r], ad = t.c->adapter[token];
     if (ad < 0) continue;
     const auto* w = static_cast<const __nv_bfloat16*>(l.a[m]) + ((static_cast<int64_t>(ad) * slabs + slab) * l.r + j) * n;
@@ -621,20 +603,29 @@ __device__ void adapter_inner(const Params& p, const Tables& t, int m0, int nm) 
     float acc[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
-#pragma unroll 2
-    for (int c = lane * 8; c < n; c += 256) {
-      uint4 wv[8];
+    auto load = [&](int c, uint4& x, uint4 (&v)[8]) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) wv[k] = ldg16(w + static_cast<int64_t>(k) * n + c);
+      for (int k = 0; k < 8; ++k) v[k] = ldg16_if(w + static_cast<int64_t>(k) * n + c, c < n);
+      x = c < n ? __ldcg(reinterpret_cast<const uint4*>(src + c)) : make_uint4(0, 0, 0, 0);
+    };
+    auto add = [&](const uint4& x, const uint4 (&v)[8]) {
       float xf[8];
-      coding::bf16x8_to_f32(__ldcg(reinterpret_cast<const uint4*>(src + c)), xf);
+      coding::bf16x8_to_f32(x, xf);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         float wf[8];
-        coding::bf16x8_to_f32(wv[k], wf);
+        coding::bf16x8_to_f32(v[k], wf);
 #pragma unroll
         for (int q = 0; q < 8; ++q) acc[k] = fmaf(wf[q], xf[q], acc[k]);
       }
+    };
+    uint4 x0, x1, w0[8], w1[8];
+    load(lane * 8, x0, w0);
+    for (int c = lane * 8; c < n; c += 512) {
+      load(c + 256, x1, w1);
+      add(x0, w0);
+      load(c + 512, x0, w0);
+      add(x1, w1);
     }
     float v = 0.0f;
 #pragma unroll
@@ -643,6 +634,69 @@ __device__ void adapter_inner(const Params& p, const Tables& t, int m0, int nm) 
       if (lane == k) v = s;
     }
     if (lane < 8) out[(static_cast<int64_t>(r) * nm + (m - m0)) * l.r + j + lane] = v;
+  }
+}
+
+// Epilogue warps: out[row][m][n] = scale * sum_i u[row][m][i] B_m[a][slab][n][i], a
+// warp per (row, pair, 128 columns): r / 8 neighbouring lanes (rounded up to a
+// power of two) take 16 bytes each of a column's row of B and add up by shuffles;
+// eight loads per lane and batch, the next batch's under way.
+__device__ void adapter_outer(const Params& p, const Tables& t, int m0, int nm) {
+  const LoraParams& l = p.a.lora;
+  const int rows = t.c->first[t.c->active], slabs = p.a.E + p.a.num_shared;
+  const int warp = (threadIdx.x >> 5) - kEpiWarp0, lane = lane_id();
+  const int n = m0 == 2 ? p.a.d : p.a.h, blocks = (n + 127) / 128;
+  const float* us = m0 == 2 ? p.u_out : p.u_in;
+  float* out = m0 == 2 ? p.d_out : p.d_in;
+  int width = 1;
+  while (width * 8 < l.r) width *= 2;  // lanes of a column
+  const int sub = lane & (width - 1), per = 32 / width, first = lane / width;
+  const bool holds = sub * 8 < l.r;
+  for (int i = blockIdx.x + gridDim.x * warp; i < rows * nm * blocks; i += gridDim.x * (kEpiThreads / 32)) {
+    const int b = i % blocks, m = m0 + (i / blocks) % nm, r = i / (blocks * nm);
+    const int ad = t.c->adapter[t.row_tok[r]];
+    if (ad < 0) continue;
+    const int64_t at = static_cast<int64_t>(r) * nm + (m - m0);
+    const int slab = t.c->slab[t.row_grp[r]], c1 = min(n, b * 128 + 128);
+    if (l.a[m] == nullptr) {
+      for (int c = b * 128 + lane; c < c1; c += 32) out[at * n + c] = 0.0f;
+      continue;
+    }
+    const auto* w = static_cast<const __nv_bfloat16*>(l.b[m]) +
+                    (static_cast<int64_t>(ad) * slabs + slab) * n * l.r + sub * 8;
+    float uf[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) uf[q] = holds ? __ldcg(us + at * l.r + sub * 8 + q) : 0.0f;
+    const float scale = __ldg(l.scale + ad);
+    auto load = [&](int c, uint4 (&v)[8]) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int col = c + k * per;
+        v[k] = ldg16_if(w + static_cast<int64_t>(col) * l.r, holds && col < c1);
+      }
+    };
+    auto finish = [&](int c, const uint4 (&v)[8]) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float f[8], s = 0.0f;
+        coding::bf16x8_to_f32(v[k], f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s = fmaf(f[q], uf[q], s);
+        for (int off = width >> 1; off >= 1; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+        const int col = c + k * per;
+        if (sub == 0 && col < c1) out[at * n + col] = s * scale;
+      }
+    };
+    uint4 v0[8], v1[8];
+    const int batch = 8 * per;  // columns
+    load(b * 128 + first, v0);
+    for (int c = b * 128; c < c1; c += 2 * batch) {
+      load(c + batch + first, v1);
+      finish(c + first, v0);
+      if (c + batch >= c1) break;
+      load(c + 2 * batch + first, v0);
+      finish(c + batch + first, v1);
+    }
   }
 }
 
@@ -927,31 +981,16 @@ __device__ __forceinline__ void load_sums(uint32_t taddr, int terms, float (&v)[
   }
 }
 
-// Final sums of hidden column n of row r: scales (cs0, cs1: the column's, 1
-// without E4M3 weights), adapters, bias, activation.  v0, v1: gate and up
-// (SwiGLU), or v0 alone.
-__device__ __forceinline__ float hidden_value(const Params& p, const Tables& t, int slab, int r, int n, float cs0,
-                                              float cs1, float bias, float v0, float v1) {
-  const DecodeArgs& a = p.a;
-  const bool pair = a.activation == MOE_ACT_SWIGLU;
-  if (a.terms) {
-    const float rs = t.row_scale[r];
-    v0 *= rs * cs0;
-    v1 *= rs * cs1;
+// Hidden value from a row's final sums v0, v1 (gate and up, or v0 alone): the
+// row's scale rs and the column's cs0, cs1 (1 without E4M3 weights), the
+// adapters' share d0, d1, bias, activation.
+__device__ __forceinline__ float hidden_value(bool pair, float rs, float cs0, float cs1, float bias, float v0, float v1,
+                                              float d0, float d1) {
+  v0 = fmaf(v0, rs * cs0, d0);
+  if (pair) {
+    v1 = fmaf(v1, rs * cs1, d1);
+    return v0 / (1.0f + __expf(-v0)) * v1;
   }
-  if (a.lora.n > 0) {
-    const int ad = t.c->adapter[t.row_tok[r]], slabs = a.E + a.num_shared;
-    if (ad >= 0) {
-      const float* u = p.u_in + static_cast<int64_t>(r) * 2 * a.lora.r;
-      if (pair) {
-        if (a.lora.a[0] != nullptr) v0 += adapter_delta(a.lora, 0, slabs, ad, slab, a.h, n, u);
-        if (a.lora.a[1] != nullptr) v1 += adapter_delta(a.lora, 1, slabs, ad, slab, a.h, n, u + a.lora.r);
-      } else if (a.lora.a[1] != nullptr) {
-        v0 += adapter_delta(a.lora, 1, slabs, ad, slab, a.h, n, u + a.lora.r);
-      }
-    }
-  }
-  if (pair) return v0 / (1.0f + __expf(-v0)) * v1;
   const float z = v0 + bias;
   return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
 }
@@ -979,7 +1018,8 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
   const int tiles = up_tiles_of(a);
   const int terms = a.terms == 2 ? 2 : 1, per = 8 / terms;  // tokens per 8 columns
   const int nl = q * 32 + lane;
-  bool inner_ready = a.lora.n == 0 || (a.lora.a[0] == nullptr && a.lora.a[1] == nullptr);
+  const bool outer = a.lora.n > 0 && (a.lora.a[0] != nullptr || a.lora.a[1] != nullptr);
+  bool outer_ready = !outer;
   for (int s = f.lo; s < f.hi; ++local) {
     const Unit u = unit_at(f, s);
     s += u.k1 - u.k0;
@@ -988,9 +1028,9 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
     const bool whole = u.k0 == 0 && u.k1 == f.nk;
     const int s0 = u.tile * f.nk;
     float* part = partial_of(p, f, blockIdx.x, s0);
-    if (!inner_ready) {
-      if (!epi_wait(p, kInnerUp, &c.abort)) return false;
-      inner_ready = true;
+    if (!outer_ready) {
+      if (!epi_wait(p, kOuterUp, &c.abort)) return false;
+      outer_ready = true;
     }
     const int n = hidden_col(pair, j, half, nl);
     const bool in = n < a.h;
@@ -1003,8 +1043,11 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
       }
       if (!pair) bias = __ldg(a.b_in + ch);
     }
-    auto finish = [&](int r, float v0, float v1) {
-      store_hidden(p, r, n, in, in ? hidden_value(p, t, slab, r, n, cs0, cs1, bias, v0, v1) : 0.0f);
+    auto adapted = [&](int r) { return outer && in && c.adapter[t.row_tok[r]] >= 0; };
+    auto share = [&](int r, int m) { return __ldcg(p.d_in + (static_cast<int64_t>(r) * 2 + m) * a.h + n); };
+    auto finish = [&](int r, float v0, float v1, float d0, float d1) {
+      const float rs = a.terms ? t.row_scale[r] : 1.0f;
+      store_hidden(p, r, n, in, hidden_value(pair, rs, cs0, cs1, bias, v0, v1, d0, d1));
     };
     const int acc = local & 1;
     bool failed = false;
@@ -1019,25 +1062,34 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
     const int cols = dense ? a.S : cnt;  // tokens in the tile's columns
     // SwiGLU: the two halves of the warps take alternate chunks of columns, both tiles; else one tile each
     for (int ch = pair ? half : 0; ch * per < cols; ch += pair ? 2 : 1) {
-      float v0[8], v1[8];
+      float v0[8], v1[8], d0[8], d1[8];
+      auto row_of = [&](int col) {  // the row of column col (-1: none)
+        if (col >= cols) return -1;
+        if (!dense) return row0 + col;
+        return (mask >> col) & 1 ? row0 + __popcll(mask & ((uint64_t(1) << col) - 1)) : -1;
+      };
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        d0[i] = d1[i] = 0.0f;
+        const int r = i < per ? row_of(ch * per + i) : -1;
+        if (whole && r >= 0 && adapted(r)) {
+          d0[i] = share(r, pair ? 0 : 1);
+          if (pair) d1[i] = share(r, 1);
+        }
+      }
       load_sums(tb + (pair ? 0 : half * (kAccCols / 2)) + ch * 8, terms, v0);
       if (pair) load_sums(tb + kAccCols / 2 + ch * 8, terms, v1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int col = ch * per + i;
-        if (i >= per || col >= cols) break;
-        int i_row = col;
-        if (dense) {
-          if (!((mask >> col) & 1)) continue;
-          i_row = __popcll(mask & ((uint64_t(1) << col) - 1));
-        }
+        const int r = i < per ? row_of(ch * per + i) : -1;
+        if (r < 0) continue;
         if (!whole) {
-          float* o = part + i_row * 256 + nl;
+          float* o = part + (r - row0) * 256 + nl;
           o[pair ? 0 : half * 128] = v0[i];
           if (pair) o[128] = v1[i];
           continue;
         }
-        finish(row0 + i_row, v0[i], pair ? v1[i] : 0.0f);
+        finish(r, v0[i], pair ? v1[i] : 0.0f, d0[i], d1[i]);
       }
     }
     tc_fence_before();
@@ -1049,6 +1101,15 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
     const int step = pair ? 8 : 4;
     for (int i0 = pair ? half * 4 : 0; i0 < cnt; i0 += step) {
       float v0[4] = {0.f, 0.f, 0.f, 0.f}, v1[4] = {0.f, 0.f, 0.f, 0.f};
+      float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = row0 + i0 + i;
+        if (i0 + i < cnt && adapted(r)) {
+          d0[i] = share(r, pair ? 0 : 1);
+          if (pair) d1[i] = share(r, 1);
+        }
+      }
       for (int cc = c0; cc <= c1; ++cc) {
         const float* src = partial_of(p, f, cc, s0) + i0 * 256 + nl + (pair ? 0 : half * 128);
 #pragma unroll
@@ -1061,7 +1122,7 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i0 + i < cnt) finish(row0 + i0 + i, v0[i], v1[i]);
+        if (i0 + i < cnt) finish(row0 + i0 + i, v0[i], v1[i], d0[i], d1[i]);
     }
   }
   return true;
@@ -1073,85 +1134,90 @@ __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, 
   const int warp = threadIdx.x >> 5, lane = lane_id(), q = warp & 3, half = (warp - kEpiWarp0) >> 2;
   const int terms = a.terms == 2 ? 2 : 1, per = 8 / terms;
   const int nl = half * 128 + q * 32 + lane;  // this thread's column of the tile
-  const int slabs = a.E + a.num_shared;
-  const int tile_steps = c.active * f.nk;  // steps of one output tile, all groups
-  bool inner_ready = a.lora.n == 0 || a.lora.a[2] == nullptr;
-  for (int s = f.lo; s < f.hi;) {
-    const int j = s / tile_steps, s0 = j * tile_steps, s1 = s0 + tile_steps, n = j * 256 + nl;
-    const bool in = n < a.d;
-    for (int tk = 0; tk < a.S; ++tk) t.y[tk * 256 + nl] = 0.0f;
-    for (; s < f.hi && s < s1; ++local) {
-      const Unit u = unit_at(f, s);
-      s += u.k1 - u.k0;
-      const int g = u.tile - j * c.active, slab = c.slab[g], row0 = c.first[g], cnt = c.first[g + 1] - row0;
-      if (!inner_ready && u.k0 == 0) {
-        if (!epi_wait(p, kCoded, &c.abort)) return false;
-        inner_ready = true;
-      }
-      const int64_t och = static_cast<int64_t>(slab) * a.d + n;
-      const float cs = a.terms && in ? __ldg(a.s_out + och) : 1.0f;
-      const float bias = a.b_out != nullptr && in && u.k0 == 0 ? __ldg(a.b_out + och) : 0.0f;
-      const int acc = local & 1;
-      bool failed = false;
-      if (!mbar_wait(&c.tfull[acc], (local >> 1) & 1, &c.abort)) {
-        if (lane == 0) give_up(p, &c.abort);
-        failed = true;
-      }
-      if (epi_any(failed)) return false;
-      tc_fence_after();
-      const uint32_t tb = c.tmem_base + acc * kAccCols + half * (kAccCols / 2) + (static_cast<uint32_t>(q * 32) << 16);
-      for (int ch = 0; ch * per < cnt; ++ch) {
-        float v[8];
-        load_sums(tb + ch * 8, terms, v);
+  const bool outer = a.lora.n > 0 && a.lora.a[2] != nullptr;
+  bool outer_ready = !outer;
+  for (int s = f.lo; s < f.hi; ++local) {
+    const Unit u = unit_at(f, s);
+    s += u.k1 - u.k0;
+    const int j = u.tile / c.active, g = u.tile - j * c.active, slab = c.slab[g];
+    const int row0 = c.first[g], cnt = c.first[g + 1] - row0, n = j * 256 + nl;
+    const bool in = n < a.d, whole = u.k0 == 0 && u.k1 == f.nk, first = u.k0 == 0;
+    if (!outer_ready && first) {  // the tile's first steps take the adapters' share
+      if (!epi_wait(p, kOuterDown, &c.abort)) return false;
+      outer_ready = true;
+    }
+    const int64_t och = static_cast<int64_t>(slab) * a.d + n;
+    const float cs = a.terms && in ? __ldg(a.s_out + och) : 1.0f;
+    const float bias = a.b_out != nullptr && in && first ? __ldg(a.b_out + och) : 0.0f;
+    const int acc = local & 1;
+    bool failed = false;
+    if (!mbar_wait(&c.tfull[acc], (local >> 1) & 1, &c.abort)) {
+      if (lane == 0) give_up(p, &c.abort);
+      failed = true;
+    }
+    if (epi_any(failed)) return false;
+    tc_fence_after();
+    const uint32_t tb = c.tmem_base + acc * kAccCols + half * (kAccCols / 2) + (static_cast<uint32_t>(q * 32) << 16);
+    // a whole tile's sums are the expert's outputs, a part's are added up at the end
+    float* dst = whole ? p.outs + static_cast<int64_t>(row0) * a.d + n
+                       : partial_of(p, f, blockIdx.x, u.tile * f.nk) + nl;
+    const int64_t stride = whole ? a.d : 256;
+    for (int ch = 0; ch * per < cnt; ++ch) {
+      float v[8], dd[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int tk = ch * per + i;
-          if (i >= per || tk >= cnt) break;
-          const int r = row0 + tk;
-          const int tok = t.row_tok[r];
-          float o = v[i];
-          if (a.terms) o *= t.row_scale[r] * cs;
-          if (u.k0 == 0) {
-            o += bias;
-            if (in && a.lora.n > 0 && a.lora.a[2] != nullptr && c.adapter[tok] >= 0)
-              o += adapter_delta(a.lora, 2, slabs, c.adapter[tok], slab, a.d, n,
-                                 p.u_out + static_cast<int64_t>(r) * a.lora.r);
-          }
-          t.y[tok * 256 + nl] += t.row_gate[r] * o;
-        }
+      for (int i = 0; i < 8; ++i) {
+        const int tk = ch * per + i;
+        dd[i] = bias;
+        if (i < per && tk < cnt && outer && first && in && c.adapter[t.row_tok[row0 + tk]] >= 0)
+          dd[i] += __ldcg(p.d_out + static_cast<int64_t>(row0 + tk) * a.d + n);
       }
-      tc_fence_before();
-      mbar_arrive(&c.tempty[acc]);
+      load_sums(tb + ch * 8, terms, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int tk = ch * per + i;
+        if (i >= per || tk >= cnt) break;
+        const float rs = a.terms ? t.row_scale[row0 + tk] : 1.0f;
+        if (in) dst[tk * stride] = fmaf(v[i], rs * cs, dd[i]);
+      }
     }
-    if (f.lo <= s0 && f.hi >= s1) {  // the whole tile: final
-      auto* y = static_cast<__nv_bfloat16*>(a.y);
-      for (int tk = 0; tk < a.S; ++tk)
-        if (in) y[static_cast<int64_t>(tk) * a.d + n] = __float2bfloat16_rn(t.y[tk * 256 + nl]);
-      continue;
-    }
-    float* part = partial_of(p, f, blockIdx.x, s0);
-    for (int tk = 0; tk < a.S; ++tk) part[tk * 256 + nl] = t.y[tk * 256 + nl];
+    tc_fence_before();
+    mbar_arrive(&c.tempty[acc]);
   }
   return true;
 }
 
-// y = the partial tiles' sums, four columns per thread of the grid.
-__device__ void sum_partials(const Params& p, const Tables& t, const Phase& f) {
+// y[t] = sum_k gate_k * expert output of its k-th row (+ the shared expert's), four
+// columns per thread of the grid: whole tiles' outputs, or the parts of a cut tile
+// in CTA order.
+__device__ void combine(const Params& p, const Tables& t, const Phase& f) {
   const DecodeArgs& a = p.a;
-  const int quads = a.d / 4, tile_steps = t.c->active * f.nk;
+  const Ctl& c = *t.c;
+  const int quads = a.d / 4, slots = a.S * a.K;
   auto* y = static_cast<__nv_bfloat16*>(a.y);
   for (int i = blockIdx.x * kEpiThreads + threadIdx.x - 32 * kEpiWarp0; i < a.S * quads; i += gridDim.x * kEpiThreads) {
-    const int tk = i / quads, n = (i - tk * quads) * 4, s0 = n / 256 * tile_steps;
-    const int c0 = f.part_of(s0), c1 = f.part_of(s0 + tile_steps - 1);
-    if (c0 == c1) continue;  // stored by its CTA
+    const int tk = i / quads, n = (i - tk * quads) * 4, j = n / 256;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int c = c0; c <= c1; ++c) {
-      const float4 q = __ldcg(reinterpret_cast<const float4*>(partial_of(p, f, c, s0) + tk * 256 + n % 256));
-      v.x += q.x;
-      v.y += q.y;
-      v.z += q.z;
-      v.w += q.w;
+#pragma unroll 4
+    for (int k = 0; k < a.K + a.num_shared; ++k) {
+      const int r = k < a.K ? t.slot_row[tk * a.K + k] : slots + tk;
+      const int g = t.row_grp[r], s0 = (j * c.active + g) * f.nk;
+      const int c0 = f.part_of(s0), c1 = f.part_of(s0 + f.nk - 1);
+      const float gate = t.row_gate[r];
+      const float* src = c0 == c1 ? p.outs + static_cast<int64_t>(r) * a.d + n
+                                  : partial_of(p, f, c0, s0) + (r - c.first[g]) * 256 + n % 256;
+      float4 o = __ldcg(reinterpret_cast<const float4*>(src));
+      for (int cc = c0 + 1; cc <= c1; ++cc) {
+        const float4 q =
+            __ldcg(reinterpret_cast<const float4*>(partial_of(p, f, cc, s0) + (r - c.first[g]) * 256 + n % 256));
+        o.x += q.x;
+        o.y += q.y;
+        o.z += q.z;
+        o.w += q.w;
+      }
+      v.x = fmaf(gate, o.x, v.x);
+      v.y = fmaf(gate, o.y, v.y);
+      v.z = fmaf(gate, o.z, v.z);
+      v.w = fmaf(gate, o.w, v.w);
     }
     *reinterpret_cast<uint2*>(y + static_cast<int64_t>(tk) * a.d + n) =
         make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
@@ -1167,14 +1233,25 @@ __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, cons
   if (inner_up) {
     adapter_inner(p, t, 0, 2);
     epi_arrive(p, kInnerUp);
+    if (!epi_wait(p, kInnerUp, &c.abort)) return;
+    adapter_outer(p, t, 0, 2);
+    epi_arrive(p, kOuterUp);
   }
   if (!epilogue_up(p, t, up, local)) return;
   epi_arrive(p, kHidden);
   if (a.terms || inner_down) {
     if (!epi_wait(p, kHidden, &c.abort)) return;
-    if (a.terms) code_hidden(p, t);
-    if (inner_down) adapter_inner(p, t, 2, 1);
-    epi_arrive(p, kCoded);
+    if (a.terms) {
+      code_hidden(p, t);
+      epi_arrive(p, kCoded);
+    }
+    if (inner_down) {
+      adapter_inner(p, t, 2, 1);
+      epi_arrive(p, kInnerDown);
+      if (!epi_wait(p, kInnerDown, &c.abort)) return;
+      adapter_outer(p, t, 2, 1);
+      epi_arrive(p, kOuterDown);
+    }
     if (a.terms) {  // the hidden rows' scales
       if (!epi_wait(p, kCoded, &c.abort)) return;
       for (int r = threadIdx.x - 32 * kEpiWarp0; r < c.first[c.active]; r += kEpiThreads)
@@ -1185,7 +1262,7 @@ __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, cons
   if (!epilogue_down(p, t, down, local)) return;
   epi_arrive(p, kSummed);
   if (!epi_wait(p, kSummed, &c.abort)) return;
-  sum_partials(p, t, down);
+  combine(p, t, down);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -1200,12 +1277,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   t.c = reinterpret_cast<Ctl*>(at);
   t.scratch = reinterpret_cast<Scratch*>(ring);
   at += (sizeof(Ctl) + 15) & ~size_t(15);
-  t.y = reinterpret_cast<float*>(at);
-  at += static_cast<size_t>(a.S) * 256 * 4;
   const int rows = a.S * (a.K + a.num_shared);
   t.row_gate = reinterpret_cast<float*>(at);
   t.row_scale = t.row_gate + rows;
   t.row_tok = reinterpret_cast<uint16_t*>(t.row_scale + rows);
+  t.row_grp = t.row_tok + rows;
+  t.slot_row = t.row_grp + rows;
   Ctl& c = *t.c;
   const int warp = threadIdx.x >> 5;
   if (warp == 1) {
@@ -1285,6 +1362,9 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   p.hs = reinterpret_cast<float*>(ws + L.hs);
   p.u_in = reinterpret_cast<float*>(ws + L.u_in);
   p.u_out = reinterpret_cast<float*>(ws + L.u_out);
+  p.d_in = reinterpret_cast<float*>(ws + L.d_in);
+  p.d_out = reinterpret_cast<float*>(ws + L.d_out);
+  p.outs = reinterpret_cast<float*>(ws + L.outs);
   p.joins = reinterpret_cast<uint32_t*>(ws + L.joins);
   p.partial = reinterpret_cast<float*>(ws + L.partial);
   p.status = reinterpret_cast<StatusBlock*>(ws);
