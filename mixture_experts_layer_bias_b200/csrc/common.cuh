@@ -109,6 +109,15 @@ __device__ __forceinline__ uint4 ldg16_if(const void* p, bool in) {
       : "l"(p), "r"(static_cast<int>(in)));
   return r;
 }
+// The same without a condition, OFF bytes past p.
+template <int OFF>
+__device__ __forceinline__ uint4 ldg16_at(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p), "n"(OFF));
+  return r;
+}
 __device__ __forceinline__ uint2 ldg8_if(const void* p, bool in) {
   uint2 r;
   asm volatile(

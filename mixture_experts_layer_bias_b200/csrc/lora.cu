@@ -24,8 +24,6 @@ namespace moe {
 namespace {
 
 constexpr int kRows = kLoraTileRows;
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kPlanThreads = 1024;
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -144,19 +142,27 @@ __device__ __forceinline__ void meta_store(TileRows& t, const MetaRegs& m) {
 }
 
 // Inner products of one (tile, slice of K) per unit.  N = pairs * r columns in
-// blocks of 32; warp w takes block w % nb and, of the slice, every kslices-th
-// piece of 32 k, the next piece's loads under way during a piece's products; the
-// warps of a block add up in a fixed order through shared memory.
+// blocks of 32; warp w takes block w % nb and every kslices-th part of the slice,
+// pieces of 32 k with the next piece's loads under way during a piece's products;
+// the warps of a block add up in a fixed order through shared memory.  (With 16
+// warps per SM the loop is bound by its own instructions as much as by loads, so
+// the whole pieces have no conditions and constant offsets.)
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
 struct InnerShape {
   int splits;  // slices of K
-  int chunk;   // k of a slice (a multiple of 32)
+  int chunk;   // k of a slice
+  int part;    // k of a warp's part of it (a multiple of 32)
 };
 
-__global__ void __launch_bounds__(kThreads, 2) lora_inner_kernel(const LoraRowsArgs a, const InnerShape sh) {
-  __shared__ float red[kWarps][kRows][33];
+template <int W>  // warps of a CTA: 4, or 8 for more than 4 blocks of columns
+__global__ void __launch_bounds__(32 * W, 16 / W) lora_inner_kernel(const LoraRowsArgs a, const InnerShape sh) {
+  __shared__ float red[W][kRows][33];
   __shared__ TileRows meta[2];
   const int lane = lane_id(), warp = threadIdx.x >> 5, r = a.lora.r, q = lane & 3, gq = lane >> 2;
-  const int cols = a.pairs * r, nb = (cols + 31) / 32, kslices = kWarps / nb;
+  const int cols = a.pairs * r, nb = (cols + 31) / 32, kslices = W / nb;
   const int block = warp % nb, kslice = warp / nb;
   pdl_wait();
   pdl_trigger();
@@ -175,15 +181,15 @@ __global__ void __launch_bounds__(kThreads, 2) lora_inner_kernel(const LoraRowsA
         return static_cast<const __nv_bfloat16*>(a.src_shared) + static_cast<int64_t>(e.y) * a.K;
       return static_cast<const __nv_bfloat16*>(a.src) + static_cast<int64_t>(a.src_by_token ? e.y : e.x) * a.K;
     };
-    // rows of A for this lane's column of each 8-column tile of the block (nullptr: no such column or no pair)
+    // rows of A for this lane's column of each 8-column tile of the block (columns that do not exist, or whose pair does
+    // not, read another one's row and are not stored)
     const __nv_bfloat16* bp[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int col = block * 32 + j * 8 + gq, m = col / r;
-      bp[j] = nullptr;
-      if (col < cols && a.lora.a[a.m0 + m] != nullptr)
-        bp[j] = static_cast<const __nv_bfloat16*>(a.lora.a[a.m0 + m]) +
-                ((static_cast<int64_t>(tile.adapter) * a.slabs + tile.expert) * r + (col - m * r)) * a.K;
+      const int col = min(block * 32 + j * 8 + gq, cols - 1), m = col / r;
+      const void* base = a.lora.a[a.m0 + m] != nullptr ? a.lora.a[a.m0 + m] : a.lora.a[a.m0 + (m ^ 1)];
+      bp[j] = static_cast<const __nv_bfloat16*>(base) +
+              ((static_cast<int64_t>(tile.adapter) * a.slabs + tile.expert) * r + (col - m * r)) * a.K;
     }
     const bool two = tile.rows > 16;
     const __nv_bfloat16* ap[2][2];
@@ -202,15 +208,14 @@ __global__ void __launch_bounds__(kThreads, 2) lora_inner_kernel(const LoraRowsA
     struct Piece {
       uint4 a[2][2], b[4];
     };
-    auto load = [&](Piece& pc, int k) {
-      const int c = k + 8 * q;  // this lane's 8 k (K is a multiple of 8)
-      const bool in = c < k1;
+    auto load = [&](Piece& pc, auto off) {  // whole piece, `off` pieces from the pointers on
+      constexpr int kBytes = decltype(off)::value * 64;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) pc.b[j] = ldg16_if(bp[j] + c, in && bp[j] != nullptr);
+      for (int j = 0; j < 4; ++j) pc.b[j] = ldg16_at<kBytes>(bp[j]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        pc.a[i][0] = ldg16_if(ap[i][0] + c, in && (i == 0 || two));
-        pc.a[i][1] = ldg16_if(ap[i][1] + c, in && (i == 0 || two));
+        pc.a[i][0] = ldg16_at<kBytes>(ap[i][0]);
+        pc.a[i][1] = ldg16_at<kBytes>(ap[i][1]);
       }
     };
     auto products = [&](const Piece& pc) {
@@ -225,16 +230,49 @@ __global__ void __launch_bounds__(kThreads, 2) lora_inner_kernel(const LoraRowsA
         }
       }
     };
+    auto advance = [&](int k) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) bp[j] += k;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ap[i][0] += k;
+        ap[i][1] += k;
+      }
+    };
     if (kslice < kslices) {
-      const int step = kslices * 32;
+      const int kb = k0 + kslice * sh.part, ke = min(k1, kb + sh.part);  // this warp's k
+      int pieces = ke > kb ? (ke - kb) / 32 : 0;
+      const int rest = ke > kb ? (ke - kb) & 31 : 0;
+      advance(kb + 8 * q);  // this lane's 8 k of the first piece
       Piece p0, p1;
-      int k = k0 + kslice * 32;
-      if (k < k1) load(p0, k);
-      for (; k < k1; k += 2 * step) {
-        load(p1, k + step);  // past the slice: zeros
+      if (pieces > 0) load(p0, Const<0>{});
+      for (; pieces > 4; pieces -= 4) {
+        load(p1, Const<1>{});
         products(p0);
-        load(p0, k + 2 * step);
+        load(p0, Const<2>{});
         products(p1);
+        load(p1, Const<3>{});
+        products(p0);
+        load(p0, Const<4>{});
+        products(p1);
+        advance(128);
+      }
+      for (; pieces > 0; --pieces) {
+        if (pieces > 1) load(p1, Const<1>{});
+        products(p0);
+        p0 = p1;
+        advance(32);
+      }
+      if (rest) {  // the last k of K, a multiple of 8
+        const bool in = 8 * q < rest;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p0.b[j] = ldg16_if(bp[j], in);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          p0.a[i][0] = ldg16_if(ap[i][0], in);
+          p0.a[i][1] = ldg16_if(ap[i][1], in);
+        }
+        products(p0);
       }
     }
     // accumulator (i, j): rows 16 i + gq (+ 8), columns 8 j + 2 q (+ 1) of the block
@@ -247,11 +285,13 @@ __global__ void __launch_bounds__(kThreads, 2) lora_inner_kernel(const LoraRowsA
         for (int v = 0; v < 4; ++v) red[warp][i * 16 + gq + (v >> 1) * 8][j * 8 + 2 * q + (v & 1)] = acc[i][j][v];
     if (next < units) meta_store(meta[buf ^ 1], ahead);
     __syncthreads();
-    for (int i = threadIdx.x; i < tile.rows * cols; i += kThreads) {
-      const int row = i / cols, col = i - row * cols, b = col / 32;
-      float s = 0.0f;
-      for (int k = 0; k < kslices; ++k) s += red[k * nb + b][row][col - b * 32];
-      u[static_cast<int64_t>(row) * cols + col] = s;
+    for (int row = warp; row < tile.rows; row += W) {
+      for (int b = 0; b < nb; ++b) {
+        const int col = b * 32 + lane;
+        float s = 0.0f;
+        for (int k = 0; k < kslices; ++k) s += red[k * nb + b][row][lane];
+        if (col < cols) u[static_cast<int64_t>(row) * cols + col] = s;
+      }
     }
     __syncthreads();
   }
@@ -265,8 +305,11 @@ __global__ void __launch_bounds__(kThreads, 2) lora_inner_kernel(const LoraRowsA
 // columns of its rows: one 16-byte store each.
 constexpr int kOuterCols = 2048;
 
+constexpr int kOuterThreads = 128;
+constexpr int kOuterWarps = kOuterThreads / 32;
+
 template <int KSTEPS>  // 16-k steps of the rank kept in registers: r <= 16 KSTEPS
-__global__ void __launch_bounds__(kThreads, KSTEPS <= 2 ? 3 : 2) lora_outer_kernel(const LoraRowsArgs a, int splits) {
+__global__ void __launch_bounds__(kOuterThreads, KSTEPS <= 2 ? 6 : 4) lora_outer_kernel(const LoraRowsArgs a, int splits) {
   __shared__ __align__(16) __nv_bfloat16 us[2][kRows][16 * KSTEPS + 8];
   __shared__ TileRows meta[2];
   const int lane = lane_id(), warp = threadIdx.x >> 5, r = a.lora.r, q = lane & 3, gq = lane >> 2;
@@ -300,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, KSTEPS <= 2 ? 3 : 2) lora_outer_kern
       }
     };
     load_b(warp);
-    for (int i = threadIdx.x; i < a.pairs * kRows * rp; i += kThreads) {
+    for (int i = threadIdx.x; i < a.pairs * kRows * rp; i += kOuterThreads) {
       const int m = i / (kRows * rp), row = i / rp % kRows, c = i % rp;
       float s = 0.0f;
       if (row < tile.rows && c < r && a.lora.a[a.m0 + m] != nullptr) {
@@ -312,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, KSTEPS <= 2 ? 3 : 2) lora_outer_kern
     __syncthreads();
     const float scale = __ldg(a.lora.scale + tile.adapter);
     const bool two = tile.rows > 16;
-    for (int it = warp; it < items; it += kWarps) {
+    for (int it = warp; it < items; it += kOuterWarps) {
       const int m = it % a.pairs, n = n0 + it / a.pairs * 32;
       float acc[2][4][4];
 #pragma unroll
@@ -333,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, KSTEPS <= 2 ? 3 : 2) lora_outer_kern
           }
         }
       }
-      load_b(it + kWarps);
+      load_b(it + kOuterWarps);
       const int col = n + 8 * q;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -355,12 +398,21 @@ __global__ void __launch_bounds__(kThreads, KSTEPS <= 2 ? 3 : 2) lora_outer_kern
   }
 }
 
+template <int W>
+cudaError_t launch_inner(const LoraRowsArgs& a, int splits, int chunk, int nb, cudaStream_t stream) {
+  const int kslices = W / nb, part = ((chunk + kslices - 1) / kslices + 31) & ~31;
+  // the tile count is known on the device only: at most one per row
+  const int64_t units = a.max_total_rows * splits, cap = static_cast<int64_t>(16 / W) * a.num_sms;
+  return launch_pdl(lora_inner_kernel<W>, dim3(static_cast<unsigned>(units < cap ? units : cap)), dim3(32 * W), 0, stream, a,
+                    InnerShape{splits, chunk, part});
+}
+
 template <int KSTEPS>
 cudaError_t launch_outer(const LoraRowsArgs& a, int splits, cudaStream_t stream) {
   const int64_t units = a.max_total_rows * ((a.N + kOuterCols - 1) / kOuterCols);
-  const int64_t cap = static_cast<int64_t>(KSTEPS <= 2 ? 3 : 2) * a.num_sms;
-  return launch_pdl(lora_outer_kernel<KSTEPS>, dim3(static_cast<unsigned>(units < cap ? units : cap)), dim3(kThreads), 0,
-                    stream, a, splits);
+  const int64_t cap = static_cast<int64_t>(KSTEPS <= 2 ? 6 : 4) * a.num_sms;
+  return launch_pdl(lora_outer_kernel<KSTEPS>, dim3(static_cast<unsigned>(units < cap ? units : cap)), dim3(kOuterThreads),
+                    0, stream, a, splits);
 }
 
 }  // namespace
@@ -375,17 +427,15 @@ cudaError_t launch_lora_plan(const LoraPlanArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_lora_rows(const LoraRowsArgs& a, cudaStream_t stream) {
   if (a.max_total_rows <= 0) return cudaSuccess;
-  // slices of K: about two units per SM when every tile is full, at least 256 k each
+  // slices of K: about four units per SM when every tile is full, at least 256 k each
   const int64_t tiles = (a.max_total_rows + kRows - 1) / kRows;
-  int splits = static_cast<int>((2 * a.num_sms + tiles - 1) / tiles);
+  int splits = static_cast<int>((4 * a.num_sms + tiles - 1) / tiles);
   if (splits > kLoraMaxSplits) splits = kLoraMaxSplits;
   if (splits > a.K / 256) splits = a.K / 256 > 0 ? a.K / 256 : 1;
   const int chunk = ((a.K + splits - 1) / splits + 31) & ~31;
   splits = (a.K + chunk - 1) / chunk;
-  // the tile count is known on the device only: at most one per row
-  const int64_t inner = a.max_total_rows * splits, cap = 2 * a.num_sms;
-  cudaError_t e = launch_pdl(lora_inner_kernel, dim3(static_cast<unsigned>(inner < cap ? inner : cap)), dim3(kThreads), 0,
-                             stream, a, InnerShape{splits, chunk});
+  const int nb = (a.pairs * a.lora.r + 31) / 32;
+  cudaError_t e = nb <= 4 ? launch_inner<4>(a, splits, chunk, nb, stream) : launch_inner<8>(a, splits, chunk, nb, stream);
   if (e != cudaSuccess) return e;
   if (a.lora.r <= 16)
     e = launch_outer<1>(a, splits, stream);
