@@ -435,9 +435,10 @@ moe_status moe_layer_decode(const moe_desc *desc, const moe_weights *w, const mo
  * tokens.  moe_grouped_ffn_lora: moe_grouped_ffn's arguments plus lora,
  * adapter_of_token [S] and token_of_row [R] (moe_permute's output; rows with
  * -1 are not computed).  moe_layer_forward_lora: moe_layer_forward's arguments
- * plus lora and adapter_of_token; it selects on fp64 logits and keys, as
- * moe_layer_decode does (moe_route: fp32), so experts whose keys are closer than
- * fp32 tells apart may be picked differently from the staged calls.  The
+ * plus lora and adapter_of_token; where two keys are too close for fp32 sums to
+ * tell, it selects on fp64 logits and keys, as moe_layer_decode does throughout
+ * (moe_route: fp32), so such experts may be picked differently from the staged
+ * calls.  The
  * adapters' inner products A x are summed in fp32 and kept as bf16 between the
  * two products, their share of a sum is bf16.  ws: at least
  * moe_lora_workspace_size bytes, otherwise as moe_layer_forward.  reroute = 1

@@ -283,11 +283,12 @@ struct LoraCall {
   LoraPlan plan{};
   float* u = nullptr;
   void* delta = nullptr;
-  float* logits = nullptr;  // layer call: the router's fp32 logits
+  float* wsq = nullptr;  // layer call: scratch of the router
+  bool counts_zeroed = false;
 };
 
 struct LoraLayout {
-  size_t counts, tiles, list, has, u, delta, logits, total;
+  size_t counts, tiles, list, has, u, delta, wsq, total;
 };
 
 LoraLayout lora_layout(const moe_desc& d, const moe_lora& l) {
@@ -308,7 +309,7 @@ LoraLayout lora_layout(const moe_desc& d, const moe_lora& l) {
   L.has = take(rows);
   L.u = take(kLoraMaxSplits * used * pairs * l.rank * 4);
   L.delta = take(rows * cols * 2);
-  L.logits = take(d.num_experts > kRouteExactAll ? S * d.num_experts * 4 : 0);
+  L.wsq = take(d.num_experts * 4);
   L.total = o;
   return L;
 }
@@ -321,7 +322,7 @@ void lora_regions(const LoraLayout& L, void* ws, LoraCall* c) {
   c->plan.has = reinterpret_cast<uint8_t*>(base + L.has);
   c->u = reinterpret_cast<float*>(base + L.u);
   c->delta = base + L.delta;
-  c->logits = reinterpret_cast<float*>(base + L.logits);
+  c->wsq = reinterpret_cast<float*>(base + L.wsq);
 }
 
 // Checks of a moe_lora against the layer (not of device data).
@@ -541,6 +542,7 @@ moe_status ffn_impl(const moe_desc& d, const moe_weights& w, const void* x_perm,
     a.rows = Rt;
     a.max_total_rows = up.max_total_rows;
     a.plan = lora->plan;
+    a.counts_zeroed = lora->counts_zeroed;
     a.status = status;
     if (launch_lora_plan(a, st) != cudaSuccess) return MOE_ERR_CUDA;
   }
@@ -631,9 +633,8 @@ moe_status layer_impl(const moe_desc* desc, const moe_weights* w, const void* x,
   if (!record(events, 0, st)) return MOE_ERR_CUDA;
   const int terms = a_terms(d);
   if (lora != nullptr) {
-    RouteArgs a = route_args(d, w, x, nullptr, idx, gates, ws);
-    a.logits_scratch = lora->logits;
-    s = cuda_status(launch_route_exact(a, st));
+    s = cuda_status(launch_route_exact(route_args(d, w, x, nullptr, idx, gates, ws), lora->wsq, lora->plan.counts, st));
+    lora->counts_zeroed = true;
   } else {
     s = route_impl(d, w, x, nullptr, idx, gates, ws, st);
   }

@@ -42,10 +42,10 @@ struct RouteArgs {
   float* score_out;         // optional [S][E]: gate sources (logits or sigmoid scores), with cand_key_out
 };
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
-// The same selection on fp64 keys (bf16 layers; logits computed).  Up to
-// kRouteExactAll experts need no logits_scratch [S][E].
-constexpr int kRouteExactAll = 32;
-cudaError_t launch_route_exact(const RouteArgs& a, cudaStream_t stream);
+// The same selection for bf16 layers, decided by fp64 keys where fp32 ones are
+// too close to tell.  wsq: scratch [E]; zero (optional): two words set to zero on
+// the way.
+cudaError_t launch_route_exact(const RouteArgs& a, float* wsq, int* zero, cudaStream_t stream);
 // x W_r^T alone, into logits_scratch.
 cudaError_t launch_router_logits(const RouteArgs& a, cudaStream_t stream);
 
@@ -219,6 +219,7 @@ struct LoraPlanArgs {
   int64_t rows;            // rows of the row space
   int64_t max_total_rows;  // bound of the rows of all groups together
   LoraPlan plan;
+  int counts_zeroed;       // 1: an earlier kernel of the call has set counts to zero
   StatusBlock* status;
 };
 cudaError_t launch_lora_plan(const LoraPlanArgs& a, cudaStream_t stream);

@@ -14,6 +14,8 @@
 // (outer) bytes per lane: a product's sum over k does not depend on the order
 // of k, so lane quad q takes 8 (4) neighbouring k for the fragment slots that
 // the instruction gives it, the same for both operands.
+#include <algorithm>
+
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
@@ -297,24 +299,22 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lora_inner_kernel(const LoraRo
   }
 }
 
-// Outer products of one (tile, kOuterCols columns of every pair) per unit.  The
+// Outer products of one (tile, block of columns of every pair) per unit.  The
 // tile's u (the slices' sums, rounded to bf16) sits in shared memory; warp w
 // makes 32 columns of a pair at a time, the next columns' rows of B under way
 // during the products.  Its column c of the 8-column tile j stands for column 8
 // (c / 2) + 2 j + c % 2 of the 32, so that a lane ends with 8 neighbouring
 // columns of its rows: one 16-byte store each.
-constexpr int kOuterCols = 2048;
-
 constexpr int kOuterThreads = 128;
 constexpr int kOuterWarps = kOuterThreads / 32;
 
 template <int KSTEPS>  // 16-k steps of the rank kept in registers: r <= 16 KSTEPS
-__global__ void __launch_bounds__(kOuterThreads, KSTEPS <= 2 ? 6 : 4) lora_outer_kernel(const LoraRowsArgs a, int splits) {
+__global__ void __launch_bounds__(kOuterThreads, KSTEPS <= 2 ? 6 : 4) lora_outer_kernel(const LoraRowsArgs a, int splits, int block) {
   __shared__ __align__(16) __nv_bfloat16 us[2][kRows][16 * KSTEPS + 8];
   __shared__ TileRows meta[2];
   const int lane = lane_id(), warp = threadIdx.x >> 5, r = a.lora.r, q = lane & 3, gq = lane >> 2;
   const int cols = a.pairs * r, rp = 16 * KSTEPS;
-  const int blocks = (a.N + kOuterCols - 1) / kOuterCols;
+  const int blocks = (a.N + block - 1) / block;
   pdl_wait();
   pdl_trigger();
   const int units = a.plan.counts[0] * blocks;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kOuterThreads, KSTEPS <= 2 ? 6 : 4) lora_outer
   __syncthreads();
   for (int un = blockIdx.x, buf = 0; un < units; un += gridDim.x, buf ^= 1) {
     const LoraTile tile = meta[buf].tile;
-    const int n0 = un % blocks * kOuterCols, nc = min(a.N - n0, kOuterCols);
+    const int n0 = un % blocks * block, nc = min(a.N - n0, block);
     const int next = un + gridDim.x;
     MetaRegs ahead{};
     if (next < units) ahead = meta_load(a.plan, next / blocks);
@@ -409,20 +409,29 @@ cudaError_t launch_inner(const LoraRowsArgs& a, int splits, int chunk, int nb, c
 
 template <int KSTEPS>
 cudaError_t launch_outer(const LoraRowsArgs& a, int splits, cudaStream_t stream) {
-  const int64_t units = a.max_total_rows * ((a.N + kOuterCols - 1) / kOuterCols);
+  // Columns of a unit: a multiple of 128 (32 per warp), at most 2048, fewer where there are few tiles (full ones at
+  // least; a small batch has more, shorter ones): about six units per SM.
+  const int64_t tiles = (a.max_total_rows + kRows - 1) / kRows;
+  const int64_t want = (6 * a.num_sms + tiles - 1) / tiles;
+  const int block = static_cast<int>(std::min<int64_t>(2048, std::max<int64_t>(128, (a.N / want + 127) / 128 * 128)));
+  const int64_t units = a.max_total_rows * ((a.N + block - 1) / block);
   const int64_t cap = static_cast<int64_t>(KSTEPS <= 2 ? 6 : 4) * a.num_sms;
   return launch_pdl(lora_outer_kernel<KSTEPS>, dim3(static_cast<unsigned>(units < cap ? units : cap)), dim3(kOuterThreads),
-                    0, stream, a, splits);
+                    0, stream, a, splits, block);
 }
 
 }  // namespace
 
 cudaError_t launch_lora_plan(const LoraPlanArgs& a, cudaStream_t stream) {
   if (a.num_groups <= 0 || a.num_groups > gemm::kMaxGroups || a.lora.n > kLoraMaxAdapters) return cudaErrorInvalidValue;
-  cudaError_t e = cudaMemsetAsync(a.plan.counts, 0, 2 * sizeof(int), stream);
-  if (e != cudaSuccess) return e;
-  lora_plan_kernel<<<a.num_groups, kPlanThreads, 0, stream>>>(a);  // (behind a memset: no dependent launch)
-  return cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  if (!a.counts_zeroed) {
+    if ((e = cudaMemsetAsync(a.plan.counts, 0, 2 * sizeof(int), stream)) != cudaSuccess) return e;
+    lora_plan_kernel<<<a.num_groups, kPlanThreads, 0, stream>>>(a);  // (behind a memset: no dependent launch)
+  } else {
+    e = launch_pdl(lora_plan_kernel, dim3(a.num_groups), dim3(kPlanThreads), 0, stream, a);
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_lora_rows(const LoraRowsArgs& a, cudaStream_t stream) {

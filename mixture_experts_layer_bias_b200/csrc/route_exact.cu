@@ -1,39 +1,41 @@
-// Router selection on fp64 keys for any number of tokens, a warp per token.
+// Router selection that two experts leave only in the order of their exact keys,
+// for any number of tokens.
 //
-// A product of two bf16 numbers is exact in fp64, so their fp64 sum gives each
-// logit to about 2^-52 of its terms: two experts change places only where the
-// exact keys do.  Up to 32 experts, every logit is summed that way, a CTA per 4
-// tokens: its four warps split d and take 4 tokens x 4 experts at a time, 16
-// fp64 multiply-adds for 4 conversions of tokens and 4 of weights, these by
-// integer operations (the conversion instruction, 16 a clock and SM, would bound
-// a dot product on its own).  Above, the fp32 logits of the tensor-core
-// GEMM select the K + 1 best experts first; those, and every expert that the
-// GEMM's error bound leaves within reach of the last of them, get exact logits,
-// and the selection and the gates are made from the exact ones only: K + 1 dot
-// products a token instead of E.
+// The logits are tensor-core products (m16n8k16, fp32 sums): a CTA takes 16
+// tokens, its eight warps split d and add up in warp order, so a sum is only
+// d / 128 + 8 additions long.  Each warp then selects two of the tokens in fp32.
+// Where two of a token's K + 1 best keys (or the last kept and the first dropped
+// group) lie closer than a bound on those sums' errors allows to tell, it selects
+// in fp64, with the logits of the experts in question summed again in fp64 (a
+// product of two bf16 numbers is exact in fp32); that is a few tokens in a
+// hundred.
 //
 // Scores, selection bias, group limit and gates as in the routing kernels
 // (jsqmd.com "第11章 MoE模型推理" 11.1.1, 11.3.3; ybb.press "MoE 推理工程深层实战"
 // 2.3); ties go to the lower index, a NaN key ranks as -inf.
 #include <math.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "pdl.cuh"
+#include "route_select.cuh"
 
 namespace moe {
 
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kWarps = 4;  // and tokens of a CTA
+constexpr int kWarps = 8;
+constexpr int kTokens = 16;  // of a CTA
 
 struct ExactParams {
   int S, d, E, K, score_fn, renormalize, num_groups, topk_groups;
   float tau;
   const __nv_bfloat16* x;
   const __nv_bfloat16* w;
-  const float* approx;  // E > 32: [S][E] fp32 logits without the bias
+  const float* wsq;  // [E]: squared lengths of the router's rows
   const float* router_bias;
   const float* sel_bias;
   int32_t* topk_idx;
@@ -70,67 +72,37 @@ __device__ __forceinline__ void warp_best(double& v, int& idx) {
   }
 }
 
-// A bf16 (its bits in the upper half of `w`) as a double times 2^-896, by
-// moving its fields: exact for every finite value, subnormals included; an
-// infinity or a NaN becomes one.
-__device__ __forceinline__ double bf16_bits_to_f64(uint32_t w) {
-  uint32_t hi = (w >> 3) & 0x0FFFE000u;  // exponent and mantissa at the bottom of a double's exponent field
-  if (hi >= 0x0FF00000u) hi |= 0x7FF00000u;
-  return __hiloint2double(static_cast<int>(hi | (w & 0x80000000u)), 0);
-}
-constexpr double kUnscale = 0x1p896;
-
-// The q-th of 8 bf16 values, as the bits of a float.
-__device__ __forceinline__ uint32_t bf16_at(const uint4& v, int q) {
+// The q-th of 8 bf16 values.
+__device__ __forceinline__ float bf16_at(const uint4& v, int q) {
   const uint32_t w = q < 2 ? v.x : q < 4 ? v.y : q < 6 ? v.z : v.w;
-  return (q & 1) ? (w & 0xFFFF0000u) : (w << 16);
+  return __uint_as_float((q & 1) ? (w & 0xFFFF0000u) : (w << 16));
 }
 
-// Exact logits of n <= 4 experts e[]; with NORMS also the largest squared length
-// of their rows and that of the token (fp32: a bound needs no more).
-template <bool NORMS>
-__device__ __forceinline__ void exact_logits(const ExactParams& p, const __nv_bfloat16* xr, const int (&e)[4], int n,
-                                             double (&out)[4], float* wnorm, float* xnorm) {
+// fp64 logits of n <= 2 experts e[], by a warp; four steps' loads at a time.
+__device__ void exact_logits(const ExactParams& p, const __nv_bfloat16* xr, const int (&e)[2], int n, double (&out)[2]) {
   const int lane = lane_id();
-  double acc[4] = {0.0, 0.0, 0.0, 0.0};
-  float sq[4] = {0.f, 0.f, 0.f, 0.f}, xq = 0.0f;
-  const __nv_bfloat16* wr[4];
+  double acc[2] = {0.0, 0.0};
+  const __nv_bfloat16* wr[2] = {p.w + static_cast<int64_t>(e[0]) * p.d, p.w + static_cast<int64_t>(e[n - 1]) * p.d};
+  for (int c = lane * 8; c < p.d; c += 1024) {
+    uint4 x[4], w[4][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) wr[i] = p.w + static_cast<int64_t>(e[i < n ? i : 0]) * p.d;
-  uint4 xv, wv[4], xn, wn[4];  // this step's pieces and the next one's
-  auto load = [&](int c, uint4& x, uint4 (&w)[4]) {
-    x = ldg16_if(xr + c, c < p.d);
+    for (int k = 0; k < 4; ++k) {
+      x[k] = ldg16_if(xr + c + 256 * k, c + 256 * k < p.d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = ldg16_if(wr[i] + c, c < p.d && i < n);
-  };
-  auto add = [&](const uint4& x, const uint4 (&w)[4]) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const float xf = __uint_as_float(bf16_at(x, q));
-      if (NORMS) xq = fmaf(xf, xf, xq);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float wf = __uint_as_float(bf16_at(w[i], q));
-        acc[i] += static_cast<double>(__fmul_rn(xf, wf));  // the product is exact in fp32
-        if (NORMS) sq[i] = fmaf(wf, wf, sq[i]);
-      }
+      for (int i = 0; i < 2; ++i) w[k][i] = ldg16_if(wr[i] + c + 256 * k, c + 256 * k < p.d);
     }
-  };
-  load(lane * 8, xv, wv);
-  for (int c = lane * 8; c < p.d; c += 512) {
-    load(c + 256, xn, wn);
-    add(xv, wv);
-    load(c + 512, xv, wv);
-    add(xn, wn);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          acc[i] += static_cast<double>(__fmul_rn(bf16_at(x[k], q), bf16_at(w[k][i], q)));
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i < n) {
+  for (int i = 0; i < 2; ++i)
+    if (i < n)
       out[i] = warp_sum_d(acc[i]) + (p.router_bias != nullptr ? static_cast<double>(__ldg(p.router_bias + e[i])) : 0.0);
-      if (NORMS) *wnorm = fmaxf(*wnorm, warp_sum_f(sq[i]));
-    }
-  }
-  if (NORMS) *xnorm = warp_sum_f(xq);
 }
 
 template <int NI>
@@ -220,119 +192,279 @@ __device__ void group_limit(const ExactParams& p, const double (&key)[NI], bool 
   for (int i = 0; i < NI; ++i) cand[i] = cand[i] && chosen[i];
 }
 
-// Logits of the CTA's 4 tokens against all experts (at most 32), into out[4][E].
-__device__ void all_logits(const ExactParams& p, int t0, double (*part)[16], double* out) {
-  const int warp = threadIdx.x >> 5, lane = lane_id();
-  const __nv_bfloat16* xr[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) xr[i] = p.x + static_cast<int64_t>(min(t0 + i, p.S - 1)) * p.d;
-  for (int e0 = 0; e0 < p.E; e0 += 4) {
-    const __nv_bfloat16* wr[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) wr[i] = p.w + static_cast<int64_t>(min(e0 + i, p.E - 1)) * p.d;
-    double acc[16];  // [token][expert]
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.0;
-    for (int c = (warp * 32 + lane) * 8; c < p.d; c += kWarps * 256) {
-      uint4 xv[4], wv[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) xv[i] = ldg16_if(xr[i] + c, true);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) wv[i] = ldg16_if(wr[i] + c, true);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        double xd[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) xd[i] = static_cast<double>(__uint_as_float(bf16_at(xv[i], q)));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const double wd = bf16_bits_to_f64(bf16_at(wv[j], q));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i * 4 + j] = fma(xd[i], wd, acc[i * 4 + j]);
-        }
-      }
-    }
-    // reduce-scatter over the warp: lanes i and i + 16 end with the warp's sum of value i
-#pragma unroll
-    for (int s = 8; s >= 1; s >>= 1) {
-      const bool upper = (lane & s) != 0;
-#pragma unroll
-      for (int i = 0; i < s; ++i) {
-        const double send = upper ? acc[i] : acc[i + s], keep = upper ? acc[i + s] : acc[i];
-        acc[i] = keep + __shfl_xor_sync(kFull, send, s);
-      }
-    }
-    acc[0] += __shfl_xor_sync(kFull, acc[0], 16);
-    if (lane < 16) part[warp][lane] = acc[0];
-    __syncthreads();
-    if (threadIdx.x < 16) {
-      const int e = e0 + (lane & 3);
-      if (e < p.E)
-        out[(lane >> 2) * p.E + e] = ((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane])) * kUnscale +
-                                     (p.router_bias != nullptr ? static_cast<double>(__ldg(p.router_bias + e)) : 0.0);
-    }
-    __syncthreads();
-  }
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int NI>
-__global__ void __launch_bounds__(kWarps * 32, NI <= 2 ? 5 : 4) route_exact_kernel(const ExactParams p) {
-  __shared__ double part[kWarps][16];
-  __shared__ double direct[kWarps * kRouteExactAll];
-  const int lane = lane_id();
-  const int tok = blockIdx.x * kWarps + (threadIdx.x >> 5);
+// Squared lengths of the router's rows, a warp per row; `zero` (optional): two
+// words that a later kernel of the call counts in.
+__global__ void __launch_bounds__(128) router_norm_kernel(const __nv_bfloat16* w, int E, int d, float* wsq, int* zero) {
+  const int e = blockIdx.x * 4 + (threadIdx.x >> 5);
   pdl_wait();
   pdl_trigger();
-  if (NI == 1) all_logits(p, blockIdx.x * kWarps, part, direct);
-  if (tok >= p.S) return;
+  if (zero != nullptr && blockIdx.x == 0 && threadIdx.x < 2) zero[threadIdx.x] = 0;
+  if (e >= E) return;
+  float sq = 0.0f;
+#pragma unroll 4
+  for (int c = lane_id() * 8; c < d; c += 256) {
+    const uint4 v = ldg16(w + static_cast<int64_t>(e) * d + c);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sq = fmaf(bf16_at(v, q), bf16_at(v, q), sq);
+  }
+  sq = warp_sum_f(sq);
+  if (lane_id() == 0) wsq[e] = sq;
+}
+
+// fp32 logits of the CTA's tokens against NT tiles of 8 experts from e0 on, into
+// out[16][E], and on the way the tokens' squared lengths.  A piece is 32 columns
+// of d (quad lane q takes columns 8 q ..: the order of a sum's terms is free),
+// the next pieces' loads under way during a piece's products.
+template <int NT>
+__device__ void tile_logits(const ExactParams& p, int t0, int e0, float (*part)[kTokens][64], float (*sq)[kTokens],
+                            float* out) {
+  const int warp = threadIdx.x >> 5, lane = lane_id(), q = lane & 3, g = lane >> 2;
+  const __nv_bfloat16 *ap[2], *bp[NT];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) ap[i] = p.x + static_cast<int64_t>(min(t0 + g + 8 * i, p.S - 1)) * p.d;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) bp[j] = p.w + static_cast<int64_t>(min(e0 + 8 * j + g, p.E - 1)) * p.d;
+  float acc[NT][4], xs[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[j][v] = 0.0f;
+  struct Piece {
+    uint4 a[2], b[NT];
+  };
+  auto load = [&](Piece& pc, int k) {
+    const bool in = k + 8 * q < p.d;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) pc.a[i] = ldg16_if(ap[i] + k + 8 * q, in);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) pc.b[j] = ldg16_if(bp[j] + k + 8 * q, in);
+  };
+  auto add = [&](const Piece& pc) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int v = 0; v < 8; ++v) xs[i] = fmaf(bf16_at(pc.a[i], v), bf16_at(pc.a[i], v), xs[i]);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      mma_bf16(acc[j], pc.a[0].x, pc.a[1].x, pc.a[0].y, pc.a[1].y, pc.b[j].x, pc.b[j].y);
+      mma_bf16(acc[j], pc.a[0].z, pc.a[1].z, pc.a[0].w, pc.a[1].w, pc.b[j].z, pc.b[j].w);
+    }
+  };
+  constexpr int kAhead = NT <= 2 ? 4 : 2;  // pieces in flight
+  Piece pc[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i) load(pc[i], (warp + i * kWarps) * 32);
+  for (int k = warp * 32; k < p.d; k += 32 * kAhead * kWarps) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      load(pc[(i + kAhead - 1) % kAhead], k + (i + kAhead - 1) * 32 * kWarps);
+      add(pc[i]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) part[warp][g + 8 * (v >> 1)][8 * j + 2 * q + (v & 1)] = acc[j][v];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    xs[i] += __shfl_xor_sync(kFull, xs[i], 1);
+    xs[i] += __shfl_xor_sync(kFull, xs[i], 2);
+    if (q == 0) sq[warp][g + 8 * i] = xs[i];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kTokens * 8 * NT; i += 32 * kWarps) {
+    const int t = i / (8 * NT), c = i % (8 * NT);
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += part[w][t][c];
+    if (e0 + c < p.E) out[t * p.E + e0 + c] = s;
+  }
+  __syncthreads();
+}
+
+// Bound on the errors of a token's fp32 logits: a sum has d / 128 + 8 additions
+// (16 products at a time in the tensor cores), each off by at most 2^-22 of its
+// largest part, which is at most |x| |w|.  Twice that.
+__device__ __forceinline__ float logit_tol(const ExactParams& p, float xsq) {
+  float w = 0.0f;
+  for (int e = lane_id(); e < p.E; e += 32) w = fmaxf(w, __ldg(p.wsq + e));
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) w = fmaxf(w, __shfl_xor_sync(kFull, w, off));
+  return 2.0f * static_cast<float>(p.d / 128 + 16) * 0x1p-22f * sqrtf(xsq * w);
+}
+
+// The token's selection by one warp, from its fp32 logits (without the bias), in
+// fp32; false, with nothing written, where that cannot tell.
+template <int NI>
+__device__ bool select_fast(const ExactParams& p, int tok, const float* approx, float tol) {
+  using namespace route_detail;
+  const int lane = lane_id();
+  const float kNegInf = __int_as_float(0xff800000);
+  float score[NI], key[NI];
+  bool valid[NI], cand[NI];
+  bool bad = false;
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int e = 32 * i + lane;
+    valid[i] = e < p.E;
+    float l = kNegInf;
+    if (valid[i]) {
+      l = approx[e];
+      if (p.router_bias != nullptr) l += __ldg(p.router_bias + e);
+      bad |= !isfinite(l);
+    }
+    score[i] = p.score_fn == MOE_SCORE_SIGMOID ? 1.0f / (1.0f + expf(-l)) : p.tau == 1.0f ? l : l / p.tau;
+    key[i] = score[i];
+    if (valid[i] && p.sel_bias != nullptr) key[i] += __ldg(p.sel_bias + e);
+    if (!valid[i]) key[i] = kNegInf;
+    bad |= valid[i] && !isfinite(key[i]);
+    cand[i] = valid[i];
+    if (valid[i]) top = fmaxf(top, fabsf(key[i]) + fabsf(l));
+  }
+  if (__any_sync(kFull, bad)) return false;
+  // a key's error: the logit's, and the roundings of the bias, the score and the selection bias
+  const float err = tol * (p.score_fn == MOE_SCORE_SIGMOID ? 0.25f : 1.0f / p.tau) + warp_max(top) * 0x1p-21f;
+  if (p.num_groups > 1) {
+    const int gs = p.E / p.num_groups;
+    float sum[NI];
+    if (gs >= 32) {
+      const int r = gs >> 5;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) sum[i] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const float s = warp_sum(valid[i] ? key[i] : 0.0f);
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+          if (j / r == i / r) sum[j] += s;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        float s = key[i];
+        for (int off = gs >> 1; off >= 1; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+        sum[i] = s;
+      }
+    }
+    float last = 0.0f;
+    uint32_t chosen = 0;
+    for (int round = 0; round <= p.topk_groups && round < p.num_groups; ++round) {
+      float bv = kNegInf;
+      int bg = 0x7fffffff;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int g = (32 * i + lane) / gs;
+        if (valid[i] && !((chosen >> i) & 1u) && (sum[i] > bv || (sum[i] == bv && g < bg))) {
+          bv = sum[i];
+          bg = g;
+        }
+      }
+      warp_argmax(bv, bg);
+      if (round == p.topk_groups) {
+        // sums of gs keys, with the roundings of their own additions
+        if (last - bv <= 4.0f * gs * err) return false;
+        break;
+      }
+      last = bv;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if ((32 * i + lane) / gs == bg) chosen |= 1u << i;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) cand[i] = cand[i] && ((chosen >> i) & 1u);
+  }
+  int my_e = 0;
+  float mine = 0.0f, last = 0.0f;
+  for (int k = 0; k <= p.K; ++k) {
+    float bv = kNegInf;
+    int be = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int e = 32 * i + lane;
+      if (cand[i] && (key[i] > bv || (key[i] == bv && e < be))) {
+        bv = key[i];
+        be = e;
+      }
+    }
+    warp_argmax(bv, be);
+    if (be >= p.E) break;  // fewer than K + 1 candidates
+    if (k > 0 && last - bv <= 2.0f * err) return false;
+    last = bv;
+    float sc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (32 * i + lane == be) {
+        cand[i] = false;
+        sc = score[i];
+      }
+    sc = __shfl_sync(kFull, sc, be & 31);
+    if (lane == k) {
+      my_e = be;
+      mine = sc;
+    }
+  }
+  const bool in = lane < p.K;
+  const float g = gate_of<NI>(score, valid, mine, in, p.score_fn, p.renormalize);
+  if (in) {
+    p.topk_idx[static_cast<int64_t>(tok) * p.K + lane] = my_e;
+    p.topk_w[static_cast<int64_t>(tok) * p.K + lane] = g;
+  }
+  return true;
+}
+
+// The same in fp64, with exact logits of everyone who is in question.
+template <int NI>
+__device__ __noinline__ void select_token(const ExactParams& p, int tok, const float* approx, float err) {
+  const int lane = lane_id();
   const __nv_bfloat16* xr = p.x + static_cast<int64_t>(tok) * p.d;
   Token<NI> t;
   t.exact = 0;
-  auto all_exact = [&]() {
-    for (int e0 = 0; e0 < p.E; e0 += 4) {
-      const int n = min(4, p.E - e0);
-      const int e[4] = {e0, e0 + 1, e0 + 2, e0 + 3};
-      double v[4];
-      exact_logits<false>(p, xr, e, n, v, nullptr, nullptr);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n) put<NI>(t, e[i], v[i]);
-    }
-  };
   double key[NI];
   bool cand[NI], valid[NI];
   double gap;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    valid[i] = 32 * i + lane < p.E;
+    const int e = 32 * i + lane;
+    valid[i] = e < p.E;
     t.logit[i] = neg_inf();
-  }
-  if (NI == 1) {
-    if (valid[0]) t.logit[0] = direct[(threadIdx.x >> 5) * p.E + lane];
-    t.exact = 1;
-  } else {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int e = 32 * i + lane;
-      if (valid[i]) {
-        t.logit[i] = static_cast<double>(__ldg(p.approx + static_cast<int64_t>(tok) * p.E + e));
-        if (p.router_bias != nullptr) t.logit[i] += static_cast<double>(__ldg(p.router_bias + e));
-        bad |= !isfinite(t.logit[i]);
-      }
+    if (valid[i]) {
+      t.logit[i] = static_cast<double>(approx[e]);
+      if (p.router_bias != nullptr) t.logit[i] += static_cast<double>(__ldg(p.router_bias + e));
+      bad |= !isfinite(t.logit[i]);
     }
-    // a token with an infinity or a NaN keeps the GEMM's logits: none of its sums means more
-    if (!__any_sync(kFull, bad)) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        cand[i] = valid[i];
-        key[i] = valid[i] ? key_of(p, t.logit[i], 32 * i + lane) : neg_inf();
+    cand[i] = valid[i];
+    key[i] = valid[i] ? key_of(p, t.logit[i], e) : neg_inf();
+  }
+  bool settled = false;  // cand holds everyone who may be picked
+  // a token with an infinity or a NaN keeps these logits: none of its sums means more
+  if (!__any_sync(kFull, bad)) {
+    group_limit<NI>(p, key, cand, &gap);
+    const double slope = p.score_fn == MOE_SCORE_SIGMOID ? 0.25 : 1.0 / static_cast<double>(p.tau);
+    const double tol = slope * static_cast<double>(err);
+    if (gap <= 2.0 * tol * (p.E / p.num_groups)) {
+      // which groups are kept is open: every expert's exact logit
+      for (int e0 = 0; e0 < p.E; e0 += 2) {
+        const int n = min(2, p.E - e0);
+        const int e[2] = {e0, min(e0 + 1, p.E - 1)};
+        double v[2];
+        exact_logits(p, xr, e, n, v);
+        put<NI>(t, e[0], v[0]);
+        if (n == 2) put<NI>(t, e[1], v[1]);
       }
-      group_limit<NI>(p, key, cand, &gap);
-      // exact logits of the K + 1 best by the GEMM's logits
-      float xn = 0.0f, wn = 0.0f;
+    } else {
+      // the K + 1 best keys, and everyone else who might beat the last of them
       double last = neg_inf();
-      int pend[4] = {0, 0, 0, 0}, np = 0;
       uint32_t taken = 0;
       for (int k = 0; k <= p.K; ++k) {
         double bv = neg_inf();
@@ -346,78 +478,68 @@ __global__ void __launch_bounds__(kWarps * 32, NI <= 2 ? 5 : 4) route_exact_kern
           }
         }
         warp_best(bv, be);
-        const bool found = be < p.E;
-        if (found) {
-#pragma unroll
-          for (int i = 0; i < NI; ++i)
-            if (32 * i + lane == be) taken |= 1u << i;
-          last = bv;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i == np) pend[i] = be;
-          ++np;
-        }
-        if (np == 4 || ((k == p.K || !found) && np > 0)) {
-          double v[4];
-          if (k < 4)
-            exact_logits<true>(p, xr, pend, np, v, &wn, &xn);
-          else
-            exact_logits<false>(p, xr, pend, np, v, nullptr, nullptr);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < np) put<NI>(t, pend[i], v[i]);
-          np = 0;
-        }
-        if (!found) break;
-      }
-      // The GEMM adds d / 16 products of 16 terms, each addition off by at most 2^-23 of the sum's largest part, which
-      // is at most |x| |w|; the first picks' row lengths stand for all rows'.  Twice that, in the key's units.
-      const double slope = p.score_fn == MOE_SCORE_SIGMOID ? 0.25 : 1.0 / static_cast<double>(p.tau);
-      const double tol = 2.0 * slope * (p.d / 16 + 16) * 0x1p-23 * sqrt(static_cast<double>(xn) * wn);
-      if (gap <= 2.0 * tol * (p.E / p.num_groups)) {
-        all_exact();
-      } else {
-        // everyone else who might beat the last of them
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          uint32_t near = __ballot_sync(kFull, cand[i] && !((taken >> i) & 1u) && key[i] >= last - 2.0 * tol);
-          while (near) {
-            const int src = __ffs(near) - 1;
-            near &= near - 1;
-            const int e[4] = {32 * i + src, 0, 0, 0};
-            double v[4];
-            exact_logits<false>(p, xr, e, 1, v, nullptr, nullptr);
-            if (lane == src) {
-              t.logit[i] = v[0];
-              t.exact |= 1u << i;
-            }
-          }
-        }
-        // experts whose logits stayed approximate are out of the running
+        if (be >= p.E) break;
+        last = bv;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-          if (!((t.exact >> i) & 1u)) cand[i] = false;
+          if (32 * i + lane == be) taken |= 1u << i;
       }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) cand[i] = cand[i] && (((taken >> i) & 1u) || key[i] >= last - 2.0 * tol);
+      // of those, the ones closer to another than their errors: only their logits are in question
+      uint32_t open = 0;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        uint32_t left = __ballot_sync(kFull, cand[i]);
+        while (left) {
+          const int src = __ffs(left) - 1;
+          left &= left - 1;
+          const double k = __shfl_sync(kFull, key[i], src);
+#pragma unroll
+          for (int m = 0; m < NI; ++m)
+            if (cand[m] && !(m == i && lane == src) && fabs(key[m] - k) <= 2.0 * tol) open |= 1u << m;
+        }
+      }
+      int pend[2] = {0, 0}, np = 0;
+      auto flush = [&]() {
+        if (np == 0) return;
+        double v[2];
+        exact_logits(p, xr, pend, np, v);
+        put<NI>(t, pend[0], v[0]);
+        if (np == 2) put<NI>(t, pend[1], v[1]);
+        np = 0;
+      };
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        uint32_t left = __ballot_sync(kFull, (open >> i) & 1u);
+        while (left) {
+          const int e = 32 * i + __ffs(left) - 1;
+          left &= left - 1;
+          if (np == 0)
+            pend[0] = e;
+          else
+            pend[1] = e;
+          if (++np == 2) flush();
+        }
+      }
+      flush();
+      settled = true;
     }
   }
-  // selection from what is exact
   double score[NI];
   bool some[NI];
   bad = false;
-  bool refined = false;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     bad |= valid[i] && !isfinite(t.logit[i]);
     score[i] = score_of(p, t.logit[i]);
     key[i] = valid[i] ? key_of(p, t.logit[i], 32 * i + lane) : neg_inf();
-    refined |= valid[i] && !((t.exact >> i) & 1u);
   }
   bad = __any_sync(kFull, bad);
-  refined = __any_sync(kFull, refined) && !bad;  // some logits are approximate: cand holds the exact ones of the kept groups
   if (bad && lane == 0) report(p.status, MOE_STATUS_NONFINITE_LOGIT, MOE_CNT_NONFINITE);
 #pragma unroll
-  for (int i = 0; i < NI; ++i) some[i] = refined ? cand[i] : valid[i];
-  if (!refined) group_limit<NI>(p, key, some, &gap);
+  for (int i = 0; i < NI; ++i) some[i] = settled ? cand[i] : valid[i];
+  if (!settled) group_limit<NI>(p, key, some, &gap);
   if (p.cand_key != nullptr) {
     // re-routing looks at every candidate: the kept groups' experts, exact or not
     bool in[NI];
@@ -491,24 +613,64 @@ __global__ void __launch_bounds__(kWarps * 32, NI <= 2 ? 5 : 4) route_exact_kern
 }
 
 template <int NI>
+__global__ void __launch_bounds__(32 * kWarps, 2) route_exact_kernel(const ExactParams p) {
+  __shared__ float part[kWarps][kTokens][64];
+  __shared__ float sq[kWarps][kTokens];
+  extern __shared__ float logits[];  // [16][E]
+  const int warp = threadIdx.x >> 5, t0 = blockIdx.x * kTokens;
+  pdl_wait();
+  pdl_trigger();
+  for (int e0 = 0; e0 < p.E; e0 += 64) {
+    const int left = p.E - e0;
+    if (NI == 1 && left <= 8)
+      tile_logits<1>(p, t0, e0, part, sq, logits);
+    else if (left <= 16)
+      tile_logits<2>(p, t0, e0, part, sq, logits);
+    else if (left <= 32)
+      tile_logits<4>(p, t0, e0, part, sq, logits);
+    else
+      tile_logits<8>(p, t0, e0, part, sq, logits);
+  }
+  for (int i = warp; i < kTokens; i += kWarps) {
+    if (t0 + i >= p.S) break;
+    float xsq = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) xsq += sq[w][i];
+    const float tol = logit_tol(p, xsq);
+    // (re-routing reads every candidate's key: the fp64 path writes them)
+    if (p.cand_key != nullptr || !select_fast<NI>(p, t0 + i, logits + i * p.E, tol))
+      select_token<NI>(p, t0 + i, logits + i * p.E, tol);
+  }
+}
+
+template <int NI>
 cudaError_t launch_ni(const ExactParams& p, cudaStream_t stream) {
-  const cudaError_t e =
-      launch_pdl(route_exact_kernel<NI>, dim3((p.S + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, stream, p);
+  if (NI == 8) {  // 16 x 256 logits beside the static arrays exceed the default 48 KB
+    static std::atomic<uint64_t> attr_set{0};  // one bit per device ordinal (host threads may launch concurrently)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(attr_set.load(std::memory_order_relaxed) & (1ull << dev))) {
+      e = cudaFuncSetAttribute(route_exact_kernel<NI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTokens * 256 * 4);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) attr_set.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+  }
+  const cudaError_t e = launch_pdl(route_exact_kernel<NI>, dim3((p.S + kTokens - 1) / kTokens), dim3(32 * kWarps),
+                                   static_cast<size_t>(kTokens) * p.E * 4, stream, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_route_exact(const RouteArgs& a, cudaStream_t stream) {
+cudaError_t launch_route_exact(const RouteArgs& a, float* wsq, int* zero, cudaStream_t stream) {
   if (a.S <= 0) return cudaSuccess;
+  const auto* w = static_cast<const __nv_bfloat16*>(a.w_router);
+  const cudaError_t e = launch_pdl(router_norm_kernel, dim3((a.E + 3) / 4), dim3(128), 0, stream, w, a.E, a.d, wsq, zero);
+  if (e != cudaSuccess) return e;
   ExactParams p{a.S, a.d, a.E, a.K, a.score_fn, a.renormalize, a.num_groups, a.topk_groups, a.tau,
-                static_cast<const __nv_bfloat16*>(a.x), static_cast<const __nv_bfloat16*>(a.w_router), nullptr,
+                static_cast<const __nv_bfloat16*>(a.x), w, wsq,
                 a.router_bias, a.sel_bias, a.topk_idx, a.topk_w, a.cand_key_out, a.score_out, a.status};
-  if (a.E > kRouteExactAll) {
-    const cudaError_t e = launch_router_logits(a, stream);
-    if (e != cudaSuccess) return e;
-    p.approx = a.logits_scratch;
-  }
   if (a.E <= 32) return launch_ni<1>(p, stream);
   if (a.E <= 64) return launch_ni<2>(p, stream);
   if (a.E <= 128) return launch_ni<4>(p, stream);
