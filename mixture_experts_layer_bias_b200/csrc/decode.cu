@@ -23,8 +23,8 @@
 // swizzle row of K (64 bf16 or 128 E4M3) of two 128-row weight tiles that share
 // one token tile: gate and up rows of the same 128 hidden columns (SwiGLU), or
 // 256 neighbouring output columns.  All steps of a phase, in the order (group,
-// tile, k) for up and (tile, group, k) for down, are cut into one equal range
-// per CTA, so every SM reads the same bytes whatever the group sizes are.  A tile
+// tile, k) for up and (tile, group, k) for down, are cut into one range of
+// equal cost per CTA (see step_cost), whatever the group sizes are.  A tile
 // cut by a range border goes through fp32 partial sums in the workspace: in the
 // up phase whichever of its CTAs arrives last joins them, in the down phase the
 // whole grid adds them at the end, together with the gate-weighted sum over a
@@ -173,9 +173,12 @@ struct Ctl {
   int active;
   int last;
   int warp_sums[kWarps];
+  int warp_costs[kWarps];
   int first[kMaxSlabs + 1];            // active group -> its first row
   int row0[kMaxSlabs];                 // slab -> its first row
   int group[kMaxSlabs];                // slab -> its active group
+  int weight[kMaxSlabs + 1];           // active group -> sum of the step costs of the groups before it
+  int begin[2][kDecodeMaxCtas + 1];    // phase, CTA -> its first step
   int slab[kMaxSlabs];                 // active group -> weight slab
   uint64_t mask[kMaxSlabs];            // active group -> its tokens
   uint64_t tokens_of[kMaxSlabs];       // slab -> its tokens
@@ -248,10 +251,9 @@ __device__ __forceinline__ bool epi_any(bool failed) {
 // (written by the generic proxy, read by other CTAs through either).
 __device__ __forceinline__ void epi_arrive(const Params& p, Arrival k) {
   fence_proxy_async_global();
-  __threadfence();
   epi_any(false);
   if (threadIdx.x == 32 * kEpiWarp0) {
-    __threadfence();
+    __threadfence();  // (the barrier before it makes this cover every warp's writes)
     atomicAdd(&p.sync->arrived[k], 1);
   }
 }
@@ -269,7 +271,6 @@ __device__ __forceinline__ bool epi_wait(const Params& p, Arrival k, volatile in
 // Every thread of every CTA: false when the wait gave up.
 __device__ bool grid_barrier(const Params& p, Ctl& c, Arrival k) {
   fence_proxy_async_global();
-  __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
@@ -429,13 +430,19 @@ __device__ void select_tokens(const Params& p, Scratch& c, int t0, int n, int wi
     if (in && !kept) c.key[tid] = 0;  // below every candidate
     __syncthreads();
   }
-  int rank = a.K;
-  if (in) {
-    const uint64_t mine = c.key[tid];
-    rank = 0;
-    for (int q = 0; q < a.E; ++q) {
-      const uint64_t o = c.key[j * width + q];
-      rank += o > mine || (o == mine && q < e);
+  const uint64_t mine_key = in ? c.key[tid] : 0;
+  if (mine_key != 0) {  // a candidate: its slot is the number of better ones
+    const uint64_t mine = mine_key;
+    int rank = 0;
+    const uint64_t* keys = c.key + j * width;
+    if (a.num_groups > 1) {
+      const int gs = a.E / a.num_groups;
+      for (int g = 0; g < a.num_groups; ++g) {
+        if (keys[g * gs] == 0) continue;  // a dropped group
+        for (int q = g * gs; q < (g + 1) * gs; ++q) rank += keys[q] > mine || (keys[q] == mine && q < e);
+      }
+    } else {
+      for (int q = 0; q < a.E; ++q) rank += keys[q] > mine || (keys[q] == mine && q < e);
     }
     if (rank < a.K) {
       idx[(t0 + j) * a.K + rank] = e;
@@ -470,6 +477,14 @@ __device__ void select_tokens(const Params& p, Scratch& c, int t0, int n, int wi
     gate[(t0 + j) * a.K + e] = g;
   }
   __syncthreads();
+}
+
+// What a step of a group with this many tokens costs: its weight bytes and, for
+// every 16 columns of its token tile, about a tenth of that again (measured on 64
+// tokens over 64 E4M3 experts: 52 us for a CTA's steps with one box of columns, 67
+// with three, 75 with five).  Groups that share a dense tile all cost the same.
+__device__ __forceinline__ int step_cost(const DecodeArgs& a, int tokens) {
+  return all_tokens(a.S, a.terms) ? 1 : 9 + (tokens * (a.terms == 2 ? 2 : 1) + 15) / 16;
 }
 
 // Selection and the group tables in this CTA's shared memory.  Up to two rounds
@@ -515,21 +530,33 @@ __device__ bool tables_phase(const Params& p, const Tables& t) {
   const uint64_t mask = tid < slabs ? c.tokens_of[tid] : 0;
   const int count = __popcll(mask);
   const int v = count | (count > 0 ? 1 << 16 : 0);
-  int incl = v;
+  const int cost = count > 0 ? step_cost(a, count) : 0;
+  int incl = v, costs = cost;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-    if (lane >= off) incl += o;
+    const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off), oc = __shfl_up_sync(0xFFFFFFFFu, costs, off);
+    if (lane >= off) {
+      incl += o;
+      costs += oc;
+    }
   }
-  if (lane == 31) c.warp_sums[warp] = incl;
+  if (lane == 31) {
+    c.warp_sums[warp] = incl;
+    c.warp_costs[warp] = costs;
+  }
   __syncthreads();
   int before = incl - v;
-  for (int w = 0; w < warp; ++w) before += c.warp_sums[w];
+  costs -= cost;
+  for (int w = 0; w < warp; ++w) {
+    before += c.warp_sums[w];
+    costs += c.warp_costs[w];
+  }
   const int row0 = before & 0xFFFF, group = before >> 16;
   if (count > 0) {
     c.first[group] = row0;
     c.slab[group] = tid;
     c.mask[group] = mask;
+    c.weight[group] = costs;
   }
   if (tid < slabs) {
     c.row0[tid] = row0;
@@ -539,6 +566,7 @@ __device__ bool tables_phase(const Params& p, const Tables& t) {
     const int all = before + v;
     c.active = all >> 16;
     c.first[all >> 16] = all & 0xFFFF;
+    c.weight[all >> 16] = costs + cost;
   }
   __syncthreads();
   for (int i = tid; i < slots + a.S * a.num_shared; i += kThreads) {
@@ -725,32 +753,82 @@ __device__ void code_hidden(const Params& p, const Tables& t) {
 }
 
 // The steps of one phase (32 bits: checked on the host), cut into `parts` ranges
-// of q or q + 1 steps, the longer ones first; this CTA's is [lo, hi).
+// of about equal cost; this CTA's is [lo, hi).
 struct Phase {
   int nk;     // steps of a tile (its K)
   int total;
   int parts;  // CTAs that have steps: every one of them at least one
-  int q, r;
+  const int* begin;
   int lo, hi;
 
-  __device__ __forceinline__ int begin_of(int c) const { return c * q + min(c, r); }
+  __device__ __forceinline__ int begin_of(int c) const { return begin[c]; }
   // the CTA whose range holds step s
   __device__ __forceinline__ int part_of(int s) const {
-    const int longer = r * (q + 1);
-    return s < longer ? s / (q + 1) : r + (s - longer) / q;
+    int a = 0, b = parts;  // begin[a] <= s < begin[b]
+    while (b - a > 1) {
+      const int m = (a + b) >> 1;
+      if (begin[m] <= s)
+        a = m;
+      else
+        b = m;
+    }
+    return a;
+  }
+  // ... and the last one of a tile's, from its first one
+  __device__ __forceinline__ int last_part(int c, int s) const {
+    while (begin[c + 1] <= s) ++c;
+    return c;
   }
 };
 
-__device__ __forceinline__ Phase phase_of(int tiles, int nk) {
+// All threads: the ranges of a phase of `tiles` tiles per group, tile after tile
+// within a group (up), or group after group within a tile (down).
+__device__ void cut_phase(Ctl& c, int ph, int tiles, int nk, bool equal) {
+  const int total = c.active * tiles * nk, parts = min(total, static_cast<int>(gridDim.x));
+  const int weight = c.weight[c.active];
+  for (int i = threadIdx.x; i <= parts; i += kThreads) {
+    int s;
+    if (equal || total < 4 * parts || i == parts) {
+      // equal costs, or too few steps to weigh them (a range must not be empty): equal numbers, the longer ones first
+      const int q = total / parts, r = total - q * parts;
+      s = i * q + min(i, r);
+    } else {
+      // the first step that starts at or after this share of the cost; a range costs at least four average steps,
+      // more than any one step
+      const int64_t all = static_cast<int64_t>(weight) * tiles * nk;
+      int64_t at = all * i / parts;
+      const int64_t row = static_cast<int64_t>(weight) * nk;  // down: one tile, all groups
+      int j = 0;
+      if (ph == 1) {
+        j = static_cast<int>(at / row);
+        at -= j * row;
+      }
+      const int64_t unit = ph == 0 ? static_cast<int64_t>(tiles) * nk : nk;  // steps of a group in a row
+      int lo = 0, hi = c.active;  // the group that holds the cost `at`
+      while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (c.weight[m] * unit <= at)
+          lo = m;
+        else
+          hi = m;
+      }
+      const int w = c.weight[lo + 1] - c.weight[lo];
+      const int64_t k = (at - c.weight[lo] * unit + w - 1) / w;
+      s = ph == 0 ? static_cast<int>(lo * unit + k) : static_cast<int>((static_cast<int64_t>(j) * c.active + lo) * nk + k);
+    }
+    c.begin[ph][i] = s;
+  }
+}
+
+__device__ __forceinline__ Phase phase_of(const Ctl& c, int ph, int tiles, int nk) {
   Phase f;
   f.nk = nk;
-  f.total = tiles * nk;
+  f.total = c.active * tiles * nk;
   f.parts = min(f.total, static_cast<int>(gridDim.x));
-  f.q = f.total / f.parts;
-  f.r = f.total - f.q * f.parts;
-  const int c = min(static_cast<int>(blockIdx.x), f.parts);
-  f.lo = f.begin_of(c);
-  f.hi = c < f.parts ? f.begin_of(c + 1) : f.lo;
+  f.begin = c.begin[ph];
+  const int i = min(static_cast<int>(blockIdx.x), f.parts);
+  f.lo = f.begin[i];
+  f.hi = i < f.parts ? f.begin[i + 1] : f.lo;
   return f;
 }
 
@@ -776,16 +854,14 @@ __device__ __forceinline__ float* partial_of(const Params& p, const Phase& f, in
 // The epilogue warps have written this CTA's part of an up tile that the CTAs
 // c0 .. c1 share: true for all of them when it was the last one.
 __device__ __forceinline__ bool join_last(const Params& p, const Tables& t, int c0, int c1) {
-  __threadfence();
   epi_any(false);
   if (threadIdx.x == 32 * kEpiWarp0) {
     __threadfence();
     t.c->last = atomicAdd(p.joins + c0, 1) == static_cast<uint32_t>(c1 - c0);
+    __threadfence();
   }
   epi_any(false);
-  const bool last = t.c->last != 0;
-  __threadfence();
-  return last;
+  return t.c->last != 0;
 }
 
 // Ring position: stage and how often the ring has gone round.
@@ -1095,7 +1171,7 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
     tc_fence_before();
     mbar_arrive(&c.tempty[acc]);
     if (whole) continue;
-    const int c0 = f.part_of(s0), c1 = f.part_of(s0 + f.nk - 1);
+    const int c0 = f.part_of(s0), c1 = f.last_part(c0, s0 + f.nk - 1);
     if (!join_last(p, t, c0, c1)) continue;
     // rows four at a time, so that their loads are in flight together
     const int step = pair ? 8 : 4;
@@ -1188,27 +1264,32 @@ __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, 
 
 // y[t] = sum_k gate_k * expert output of its k-th row (+ the shared expert's), four
 // columns per thread of the grid: whole tiles' outputs, or the parts of a cut tile
-// in CTA order.
-__device__ void combine(const Params& p, const Tables& t, const Phase& f) {
+// in CTA order.  parts (shared memory, the idle ring): each tile's first CTA, and
+// how many more hold parts of it.
+__device__ void combine(const Params& p, const Tables& t, const Phase& f, uchar2* parts) {
   const DecodeArgs& a = p.a;
   const Ctl& c = *t.c;
-  const int quads = a.d / 4, slots = a.S * a.K;
+  const int quads = a.d / 4, slots = a.S * a.K, tid = threadIdx.x - 32 * kEpiWarp0;
+  for (int i = tid; i < f.total / f.nk; i += kEpiThreads) {
+    const int c0 = f.part_of(i * f.nk);
+    parts[i] = make_uchar2(c0, f.last_part(c0, i * f.nk + f.nk - 1) - c0);
+  }
+  epi_any(false);
   auto* y = static_cast<__nv_bfloat16*>(a.y);
-  for (int i = blockIdx.x * kEpiThreads + threadIdx.x - 32 * kEpiWarp0; i < a.S * quads; i += gridDim.x * kEpiThreads) {
+  for (int i = blockIdx.x * kEpiThreads + tid; i < a.S * quads; i += gridDim.x * kEpiThreads) {
     const int tk = i / quads, n = (i - tk * quads) * 4, j = n / 256;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < a.K + a.num_shared; ++k) {
       const int r = k < a.K ? t.slot_row[tk * a.K + k] : slots + tk;
-      const int g = t.row_grp[r], s0 = (j * c.active + g) * f.nk;
-      const int c0 = f.part_of(s0), c1 = f.part_of(s0 + f.nk - 1);
+      const int g = t.row_grp[r], tile = j * c.active + g;
+      const uchar2 pt = parts[tile];
       const float gate = t.row_gate[r];
-      const float* src = c0 == c1 ? p.outs + static_cast<int64_t>(r) * a.d + n
-                                  : partial_of(p, f, c0, s0) + (r - c.first[g]) * 256 + n % 256;
+      const int64_t at = static_cast<int64_t>(r - c.first[g]) * 256 + n % 256;
+      const float* src = pt.y == 0 ? p.outs + static_cast<int64_t>(r) * a.d + n : partial_of(p, f, pt.x, tile * f.nk) + at;
       float4 o = __ldcg(reinterpret_cast<const float4*>(src));
-      for (int cc = c0 + 1; cc <= c1; ++cc) {
-        const float4 q =
-            __ldcg(reinterpret_cast<const float4*>(partial_of(p, f, cc, s0) + (r - c.first[g]) * 256 + n % 256));
+      for (int cc = 1; cc <= pt.y; ++cc) {
+        const float4 q = __ldcg(reinterpret_cast<const float4*>(partial_of(p, f, pt.x + cc, tile * f.nk) + at));
         o.x += q.x;
         o.y += q.y;
         o.z += q.z;
@@ -1224,7 +1305,7 @@ __device__ void combine(const Params& p, const Tables& t, const Phase& f) {
   }
 }
 
-__device__ void epilogue(const Params& p, const Tables& t, const Phase& up, const Phase& down) {
+__device__ void epilogue(const Params& p, const Tables& t, const Phase& up, const Phase& down, uint8_t* ring) {
   const DecodeArgs& a = p.a;
   Ctl& c = *t.c;
   int local = 0;
@@ -1262,7 +1343,7 @@ __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, cons
   if (!epilogue_down(p, t, down, local)) return;
   epi_arrive(p, kSummed);
   if (!epi_wait(p, kSummed, &c.abort)) return;
-  combine(p, t, down);
+  combine(p, t, down, reinterpret_cast<uchar2*>(ring));
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -1311,14 +1392,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (grid_barrier(p, c, kRouted) && tables_phase(p, t)) {
     const bool pair = a.activation == MOE_ACT_SWIGLU;
     const int bk = a.terms ? 128 : 64;
-    const Phase up = phase_of(c.active * up_tiles_of(a), (a.d + bk - 1) / bk);
-    const Phase down = phase_of(c.active * ((a.d + 255) / 256), (a.h + bk - 1) / bk);
+    const int up_nk = (a.d + bk - 1) / bk, down_nk = (a.h + bk - 1) / bk;
+    const bool equal = all_tokens(a.S, a.terms);
+    cut_phase(c, 0, up_tiles_of(a), up_nk, equal);
+    cut_phase(c, 1, (a.d + 255) / 256, down_nk, equal);
+    __syncthreads();
+    const Phase up = phase_of(c, 0, up_tiles_of(a), up_nk);
+    const Phase down = phase_of(c, 1, (a.d + 255) / 256, down_nk);
     if (warp == 0)
       produce(p, t, ring, up, down, &m_in0, pair ? &m_in1 : &m_in0, &m_out, &m_x, &m_hidden);
     else if (warp == 1 && lane_id() == 0)
       multiply(p, t, ring, up, down);
     else if (warp >= kEpiWarp0)
-      epilogue(p, t, up, down);
+      epilogue(p, t, up, down, ring);
     __syncwarp();
   }
   tc_fence_before();
@@ -1383,6 +1469,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   if (slabs * ((a.h + 127) / 128) * ((a.d + bk - 1) / bk) > (1 << 30) ||
       slabs * ((a.d + 255) / 256) * ((a.h + bk - 1) / bk) > (1 << 30))
     return cudaErrorInvalidValue;
+  if (2 * slabs * ((a.d + 255) / 256) > p.ring_bytes) return cudaErrorInvalidValue;  // the combine's table of tiles
   const int64_t rows = static_cast<int64_t>(a.S) * (a.K + a.num_shared);
   CUtensorMap in0, in1, out, mx, mh;
   if (!gemm::make_slab_map(&in0, a.w_in[0], slabs, a.h, a.d, eb) || !gemm::make_slab_map(&out, a.w_out, slabs, a.d, a.h, eb))
