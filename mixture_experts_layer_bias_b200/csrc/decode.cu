@@ -78,6 +78,7 @@ constexpr int kEpiThreads = kThreads - 32 * kEpiWarp0;
 constexpr int kMaxSlabs = 257;
 constexpr int kRouteTokens = 8;  // tokens per warp of the logits
 constexpr int kMaxStages = 8;
+constexpr int kMaxSlices = 8;  // of K, in the adapters' inner products
 constexpr int kTileBytes = 128 * 128;  // one weight tile of a step: 128 rows x 128 bytes of K
 constexpr int kAccCols = 256;          // TMEM columns of one accumulator pair (128 per tile), two pairs
 constexpr int kTmemCols = 512;
@@ -123,8 +124,8 @@ Ws ws_layout(int S, int d, int E, int K, int h, int ns, int terms, int rank) {
   L.amax = take(terms ? rows * 4 : 0);
   L.hq = take(static_cast<size_t>(terms) * rows * h);
   L.hs = take(terms ? rows * 4 : 0);
-  L.u_in = take(rows * 2 * rank * 4);
-  L.u_out = take(rows * rank * 4);
+  L.u_in = take(kMaxSlices * rows * 2 * rank * 4);
+  L.u_out = take(kMaxSlices * rows * rank * 4);
   L.d_in = take(rank ? rows * 2 * h * 4 : 0);
   L.d_out = take(rank ? rows * d * 4 : 0);
   L.outs = take(rows * d * 4);
@@ -147,7 +148,7 @@ struct Params {
   uint32_t* amax;
   uint8_t* hq;
   float* hs;
-  float* u_in;   // adapters: inner products [row][2][r], [row][r]
+  float* u_in;   // adapters: inner products by slice of K [slice][row][2][r], [slice][row][r]
   float* u_out;
   float* d_in;   // outer products [row][2][h], [row][d]
   float* d_out;
@@ -610,92 +611,142 @@ __device__ bool tables_phase(const Params& p, const Tables& t) {
   return grid_barrier(p, c, kPacked);
 }
 
-// Epilogue warps: u[row][m][i] = A_m[a][slab][i] . row for the pairs m0 .. m0 +
-// nm - 1, a warp per (row, pair, 8 values): the row's pieces meet eight rows of
-// A, two steps of nine loads in flight per lane.
+// This warp's share [lo, hi) of n items that the grid's epilogue warps divide.
+__device__ __forceinline__ void warp_share(int n, int& lo, int& hi) {
+  const int warps = gridDim.x * (kEpiThreads / 32), w = ((threadIdx.x >> 5) - kEpiWarp0) * gridDim.x + blockIdx.x;
+  const int q = n / warps, r = n - q * warps;
+  lo = w * q + min(w, r);
+  hi = lo + q + (w < r ? 1 : 0);
+}
+
+// Slices of K of the inner products: about two items for every warp of the grid.
+__device__ __forceinline__ int inner_slices(int items, int pieces) {
+  const int warps = gridDim.x * (kEpiThreads / 32);
+  return max(1, min(min(kMaxSlices, pieces), 2 * warps / max(items, 1)));
+}
+
+// Epilogue warps: u[slice][row][m][i] = A_m[a][slab][i] . row over a slice of K, for
+// the pairs m0 .. m0 + nm - 1.  An item is (row, pair, 8 values, slice): the row's
+// pieces of 256 meet eight rows of A, nine loads per lane and piece; a warp
+// streams through its items' pieces with the next one's loads always under way.
 __device__ void adapter_inner(const Params& p, const Tables& t, int m0, int nm) {
   const LoraParams& l = p.a.lora;
   const int rows = t.c->first[t.c->active], slabs = p.a.E + p.a.num_shared, blocks = l.r / 8;
-  const int warp = (threadIdx.x >> 5) - kEpiWarp0, lane = lane_id();
-  const int n = m0 == 2 ? p.a.h : p.a.d;
+  const int lane = lane_id();
+  const int n = m0 == 2 ? p.a.h : p.a.d, pieces = (n + 255) / 256;
   float* out = m0 == 2 ? p.u_out : p.u_in;
-  for (int i = blockIdx.x + gridDim.x * warp; i < rows * nm * blocks; i += gridDim.x * (kEpiThreads / 32)) {
-    const int j = i % blocks * 8, m = m0 + (i / blocks) % nm, r = i / (blocks * nm);
-    if (l.a[m] == nullptr) continue;
-    const int slab = t.c->slab[t.row_grp[r]];
-    const int token = t.row_tok[r], ad = t.c->adapter[token];
-    if (ad < 0) continue;
-    const auto* w = static_cast<const __nv_bfloat16*>(l.a[m]) + ((static_cast<int64_t>(ad) * slabs + slab) * l.r + j) * n;
-    const __nv_bfloat16* src = m0 == 2 ? p.hidden + static_cast<int64_t>(r) * n
-                                       : static_cast<const __nv_bfloat16*>(p.a.x) + static_cast<int64_t>(token) * n;
-    float acc[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
-    auto load = [&](int c, uint4& x, uint4 (&v)[8]) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = ldg16_if(w + static_cast<int64_t>(k) * n + c, c < n);
-      x = c < n ? __ldcg(reinterpret_cast<const uint4*>(src + c)) : make_uint4(0, 0, 0, 0);
-    };
-    auto add = [&](const uint4& x, const uint4 (&v)[8]) {
-      float xf[8];
-      coding::bf16x8_to_f32(x, xf);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float wf[8];
-        coding::bf16x8_to_f32(v[k], wf);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) acc[k] = fmaf(wf[q], xf[q], acc[k]);
-      }
-    };
-    uint4 x0, x1, w0[8], w1[8];
-    load(lane * 8, x0, w0);
-    for (int c = lane * 8; c < n; c += 512) {
-      load(c + 256, x1, w1);
-      add(x0, w0);
-      load(c + 512, x0, w0);
-      add(x1, w1);
+  const int slices = inner_slices(rows * nm * blocks, pieces);
+  int lo, hi;
+  warp_share(rows * nm * blocks * slices, lo, hi);
+  struct Cursor {
+    int item, piece, end;
+    const __nv_bfloat16 *w, *src;  // w nullptr: nothing to do for this item
+  };
+  auto seek = [&](Cursor& c) {  // to the item's rows
+    const int s = c.item % slices, i = c.item / slices;
+    const int j = i % blocks * 8, m = m0 + i / blocks % nm, r = i / (blocks * nm);
+    c.piece = pieces * s / slices;
+    c.end = pieces * (s + 1) / slices;
+    c.w = nullptr;
+    if (c.item >= hi || l.a[m] == nullptr) return;
+    const int token = t.row_tok[r], ad = t.c->adapter[token], slab = t.c->slab[t.row_grp[r]];
+    if (ad < 0) return;
+    c.w = static_cast<const __nv_bfloat16*>(l.a[m]) + ((static_cast<int64_t>(ad) * slabs + slab) * l.r + j) * n;
+    c.src = m0 == 2 ? p.hidden + static_cast<int64_t>(r) * n
+                    : static_cast<const __nv_bfloat16*>(p.a.x) + static_cast<int64_t>(token) * n;
+  };
+  auto next = [&](Cursor& c) {
+    if (++c.piece == c.end || c.w == nullptr) {
+      do {
+        ++c.item;
+        seek(c);
+      } while (c.w == nullptr && c.item < hi);
     }
+  };
+  struct Piece {
+    uint4 x, w[8];
+  };
+  auto load = [&](const Cursor& c, Piece& pc) {
+    const int col = c.piece * 256 + lane * 8;
+    const bool in = c.w != nullptr && col < n;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) pc.w[k] = ldg16_if(c.w + static_cast<int64_t>(k) * n + col, in);
+    pc.x = in ? __ldcg(reinterpret_cast<const uint4*>(c.src + col)) : make_uint4(0, 0, 0, 0);
+  };
+  float acc[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+  auto add = [&](const Cursor& c, const Piece& pc) {
+    float xf[8];
+    coding::bf16x8_to_f32(pc.x, xf);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float wf[8];
+      coding::bf16x8_to_f32(pc.w[k], wf);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[k] = fmaf(wf[q], xf[q], acc[k]);
+    }
+    if (c.piece + 1 < c.end) return;
     float v = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float s = warp_sum(acc[k]);
       if (lane == k) v = s;
+      acc[k] = 0.0f;
     }
-    if (lane < 8) out[(static_cast<int64_t>(r) * nm + (m - m0)) * l.r + j + lane] = v;
+    const int s = c.item % slices, i = c.item / slices;
+    if (lane < 8) out[(static_cast<int64_t>(s) * rows * nm + i / blocks) * l.r + i % blocks * 8 + lane] = v;
+  };
+  Cursor c0{lo, 0, 0, nullptr, nullptr};
+  if (lo < hi) seek(c0);
+  if (c0.w == nullptr) next(c0);
+  Piece p0, p1;
+  load(c0, p0);
+  while (c0.w != nullptr) {
+    Cursor c1 = c0;
+    next(c1);
+    load(c1, p1);
+    add(c0, p0);
+    if (c1.w == nullptr) break;
+    c0 = c1;
+    next(c0);
+    load(c0, p0);
+    add(c1, p1);
   }
 }
 
-// Epilogue warps: out[row][m][n] = scale * sum_i u[row][m][i] B_m[a][slab][n][i], a
-// warp per (row, pair, 128 columns): r / 8 neighbouring lanes (rounded up to a
-// power of two) take 16 bytes each of a column's row of B and add up by shuffles;
-// eight loads per lane and batch, the next batch's under way.
+// Epilogue warps: out[row][m][n] = scale * sum_i u[row][m][i] B_m[a][slab][n][i].
+// r / 8 neighbouring lanes (rounded up to a power of two) take 16 bytes each of a
+// column's row of B and add up by shuffles; eight loads per lane make a batch of
+// columns, the next batch's under way, and a warp takes an equal run of batches.
 __device__ void adapter_outer(const Params& p, const Tables& t, int m0, int nm) {
   const LoraParams& l = p.a.lora;
-  const int rows = t.c->first[t.c->active], slabs = p.a.E + p.a.num_shared;
-  const int warp = (threadIdx.x >> 5) - kEpiWarp0, lane = lane_id();
-  const int n = m0 == 2 ? p.a.d : p.a.h, blocks = (n + 127) / 128;
+  const int rows = t.c->first[t.c->active], slabs = p.a.E + p.a.num_shared, lane = lane_id();
+  const int n = m0 == 2 ? p.a.d : p.a.h;
   const float* us = m0 == 2 ? p.u_out : p.u_in;
   float* out = m0 == 2 ? p.d_out : p.d_in;
   int width = 1;
   while (width * 8 < l.r) width *= 2;  // lanes of a column
-  const int sub = lane & (width - 1), per = 32 / width, first = lane / width;
+  const int sub = lane & (width - 1), per = 32 / width, first = lane / width, batch = 8 * per;
+  const int batches = (n + batch - 1) / batch;
   const bool holds = sub * 8 < l.r;
-  for (int i = blockIdx.x + gridDim.x * warp; i < rows * nm * blocks; i += gridDim.x * (kEpiThreads / 32)) {
-    const int b = i % blocks, m = m0 + (i / blocks) % nm, r = i / (blocks * nm);
+  const int slices = inner_slices(rows * nm * (l.r / 8), ((m0 == 2 ? p.a.h : p.a.d) + 255) / 256);
+  int lo, hi;
+  warp_share(rows * nm * batches, lo, hi);
+  while (lo < hi) {
+    const int at = lo / batches, m = m0 + at % nm, r = at / nm;  // at = r * nm + m - m0
+    const int b0 = lo - at * batches, b1 = min(batches, b0 + hi - lo);
+    lo += b1 - b0;
     const int ad = t.c->adapter[t.row_tok[r]];
     if (ad < 0) continue;
-    const int64_t at = static_cast<int64_t>(r) * nm + (m - m0);
-    const int slab = t.c->slab[t.row_grp[r]], c1 = min(n, b * 128 + 128);
+    float* o = out + static_cast<int64_t>(at) * n;
+    const int c1 = min(n, b1 * batch);
     if (l.a[m] == nullptr) {
-      for (int c = b * 128 + lane; c < c1; c += 32) out[at * n + c] = 0.0f;
+      for (int c = b0 * batch + lane; c < c1; c += 32) o[c] = 0.0f;
       continue;
     }
     const auto* w = static_cast<const __nv_bfloat16*>(l.b[m]) +
-                    (static_cast<int64_t>(ad) * slabs + slab) * n * l.r + sub * 8;
-    float uf[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) uf[q] = holds ? __ldcg(us + at * l.r + sub * 8 + q) : 0.0f;
-    const float scale = __ldg(l.scale + ad);
+                    (static_cast<int64_t>(ad) * slabs + t.c->slab[t.row_grp[r]]) * n * l.r + sub * 8;
     auto load = [&](int c, uint4 (&v)[8]) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -703,6 +754,24 @@ __device__ void adapter_outer(const Params& p, const Tables& t, int m0, int nm) 
         v[k] = ldg16_if(w + static_cast<int64_t>(col) * l.r, holds && col < c1);
       }
     };
+    uint4 v0[8], v1[8];
+    load(b0 * batch + first, v0);
+    float uf[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) uf[q] = 0.0f;
+    for (int k = 0; k < slices && holds; ++k) {
+      const float* src = us + (static_cast<int64_t>(k) * rows * nm + at) * l.r + sub * 8;
+      const float4 a0 = __ldcg(reinterpret_cast<const float4*>(src)), a1 = __ldcg(reinterpret_cast<const float4*>(src + 4));
+      uf[0] += a0.x;
+      uf[1] += a0.y;
+      uf[2] += a0.z;
+      uf[3] += a0.w;
+      uf[4] += a1.x;
+      uf[5] += a1.y;
+      uf[6] += a1.z;
+      uf[7] += a1.w;
+    }
+    const float scale = __ldg(l.scale + ad);
     auto finish = [&](int c, const uint4 (&v)[8]) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -712,18 +781,14 @@ __device__ void adapter_outer(const Params& p, const Tables& t, int m0, int nm) 
         for (int q = 0; q < 8; ++q) s = fmaf(f[q], uf[q], s);
         for (int off = width >> 1; off >= 1; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
         const int col = c + k * per;
-        if (sub == 0 && col < c1) out[at * n + col] = s * scale;
+        if (sub == 0 && col < c1) o[col] = s * scale;
       }
     };
-    uint4 v0[8], v1[8];
-    const int batch = 8 * per;  // columns
-    load(b * 128 + first, v0);
-    for (int c = b * 128; c < c1; c += 2 * batch) {
-      load(c + batch + first, v1);
-      finish(c + first, v0);
-      if (c + batch >= c1) break;
-      load(c + 2 * batch + first, v0);
-      finish(c + batch + first, v1);
+    for (int c = b0 * batch + first; c - first < c1; c += 2 * batch) {
+      load(c + batch, v1);
+      finish(c, v0);
+      load(c + 2 * batch, v0);
+      finish(c + batch, v1);  // past the end: stores nothing
     }
   }
 }
