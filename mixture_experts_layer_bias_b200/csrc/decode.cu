@@ -80,8 +80,8 @@ constexpr int kRouteTokens = 8;  // tokens per warp of the logits
 constexpr int kMaxStages = 8;
 constexpr int kMaxSlices = 8;  // of K, in the adapters' inner products
 constexpr int kTileBytes = 128 * 128;  // one weight tile of a step: 128 rows x 128 bytes of K
-constexpr int kAccCols = 256;          // TMEM columns of one accumulator pair (128 per tile), two pairs
 constexpr int kTmemCols = 512;
+constexpr int kAccs = 16;  // accumulator pairs in flight, 2 x 16 .. 2 x 128 columns each
 constexpr size_t kSmemLimit = 232448;  // 227 KB per CTA
 
 // Grid-wide arrival counters, in the workspace's first 256 bytes behind the
@@ -166,9 +166,10 @@ struct Ctl {
   uint64_t full_w[kMaxStages];
   uint64_t full_b[kMaxStages];
   uint64_t empty[kMaxStages];
-  uint64_t tfull[2];
-  uint64_t tempty[2];
+  uint64_t tfull[kAccs];
+  uint64_t tempty[kAccs];
   uint64_t drain;
+  int acc_begin[kAccs], acc_end[kAccs];  // TMEM columns of the units in flight (the MMA thread's)
   uint32_t tmem_base;
   int abort;
   int active;
@@ -1058,26 +1059,57 @@ __device__ void produce(const Params& p, const Tables& t, uint8_t* ring, const P
   }
 }
 
+// TMEM columns of the units' accumulator pairs, one after another around the 512:
+// the MMA thread and the epilogue warps follow the same sequence.  Small groups
+// take few columns, so up to 16 units run ahead of the epilogue (while its warps
+// are still at the adapters' products, above all).
+struct AccRing {
+  int tail = 0;
+  __device__ __forceinline__ int take(int n) {  // n columns per tile
+    const int at = tail + 2 * n > kTmemCols ? 0 : tail;
+    tail = at + 2 * n;
+    return at;
+  }
+};
+
+// MMA columns of a group's token tile.
+__device__ __forceinline__ int tile_cols(const Params& p, const Ctl& c, int ph, int g) {
+  const int terms = p.a.terms == 2 ? 2 : 1;
+  if (ph == 0 && all_tokens(p.a.S, p.a.terms)) return 16;
+  return ((c.first[g + 1] - c.first[g]) * terms + 15) & ~15;
+}
+
 // Warp 1, one lane.
 __device__ void multiply(const Params& p, const Tables& t, uint8_t* ring, const Phase& up, const Phase& down) {
   const DecodeArgs& a = p.a;
   Ctl& c = *t.c;
-  const int tiles = up_tiles_of(a), terms = a.terms == 2 ? 2 : 1;
-  const bool dense = all_tokens(a.S, a.terms);
+  const int tiles = up_tiles_of(a);
   Slot at;
-  int local = 0;
+  AccRing ring_cols;
+  int local = 0, drained = 0;  // units issued, units whose accumulators the epilogue has read
   bool ok = true;
   for (int ph = 0; ph < 2 && ok; ++ph) {
     const Phase& f = ph == 0 ? up : down;
     for (int s = f.lo; s < f.hi && ok; ++local) {
       const Unit u = unit_at(f, s);
       const int g = ph == 0 ? u.tile / tiles : u.tile % c.active;
-      const int n = ph == 0 && dense ? 16 : ((c.first[g + 1] - c.first[g]) * terms + 15) & ~15;
+      const int n = tile_cols(p, c, ph, g);
       const uint32_t idesc = a.terms ? idesc_e4m3_f32(128, n) : idesc_bf16_f32(128, n);
-      const int acc = local & 1;
-      if (!(ok = mbar_wait(&c.tempty[acc], ((local >> 1) & 1) ^ 1u, &c.abort))) break;
+      const int acc = local % kAccs, col = ring_cols.take(n);
+      // the columns are free once every unit in flight that holds some of them has been read (oldest first)
+      while (ok) {
+        bool free = local - drained < kAccs;
+        for (int o = drained; o < local && free; ++o)
+          free = c.acc_end[o % kAccs] <= col || c.acc_begin[o % kAccs] >= col + 2 * n;
+        if (free) break;
+        ok = mbar_wait(&c.tempty[drained % kAccs], (drained / kAccs) & 1, &c.abort);
+        ++drained;
+      }
+      if (!ok) break;
+      c.acc_begin[acc] = col;
+      c.acc_end[acc] = col + 2 * n;
       tc_fence_after();
-      const uint32_t d0 = c.tmem_base + acc * kAccCols, d1 = d0 + kAccCols / 2;
+      const uint32_t d0 = c.tmem_base + col, d1 = d0 + n;
       for (int k = u.k0; k < u.k1; ++k) {
         if (!(ok = mbar_wait(&c.full_w[at.stage], at.round, &c.abort))) break;
         if (!(ok = mbar_wait(&c.full_b[at.stage], at.round, &c.abort))) break;
@@ -1151,7 +1183,7 @@ __device__ __forceinline__ void store_hidden(const Params& p, int r, int n, bool
 // One hidden element of a tile: tile column `n` (0..127) of half `m`.
 __device__ __forceinline__ int hidden_col(bool pair, int j, int m, int n) { return pair ? j * 128 + n : j * 256 + m * 128 + n; }
 
-__device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, int& local) {
+__device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, int& local, AccRing& cols_ring) {
   const DecodeArgs& a = p.a;
   Ctl& c = *t.c;
   const int warp = threadIdx.x >> 5, lane = lane_id(), q = warp & 3, half = (warp - kEpiWarp0) >> 2;
@@ -1190,15 +1222,15 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
       const float rs = a.terms ? t.row_scale[r] : 1.0f;
       store_hidden(p, r, n, in, hidden_value(pair, rs, cs0, cs1, bias, v0, v1, d0, d1));
     };
-    const int acc = local & 1;
+    const int acc = local % kAccs, acc_n = tile_cols(p, c, 0, g), acc_col = cols_ring.take(acc_n);
     bool failed = false;
-    if (!mbar_wait(&c.tfull[acc], (local >> 1) & 1, &c.abort)) {
+    if (!mbar_wait(&c.tfull[acc], (local / kAccs) & 1, &c.abort)) {
       if (lane == 0) give_up(p, &c.abort);
       failed = true;
     }
     if (epi_any(failed)) return false;
     tc_fence_after();
-    const uint32_t tb = c.tmem_base + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t tb = c.tmem_base + acc_col + (static_cast<uint32_t>(q * 32) << 16);
     const uint64_t mask = c.mask[g];
     const int cols = dense ? a.S : cnt;  // tokens in the tile's columns
     // SwiGLU: the two halves of the warps take alternate chunks of columns, both tiles; else one tile each
@@ -1218,8 +1250,8 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
           if (pair) d1[i] = share(r, 1);
         }
       }
-      load_sums(tb + (pair ? 0 : half * (kAccCols / 2)) + ch * 8, terms, v0);
-      if (pair) load_sums(tb + kAccCols / 2 + ch * 8, terms, v1);
+      load_sums(tb + (pair ? 0 : half * acc_n) + ch * 8, terms, v0);
+      if (pair) load_sums(tb + acc_n + ch * 8, terms, v1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = i < per ? row_of(ch * per + i) : -1;
@@ -1269,7 +1301,7 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
   return true;
 }
 
-__device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, int& local) {
+__device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, int& local, AccRing& cols_ring) {
   const DecodeArgs& a = p.a;
   Ctl& c = *t.c;
   const int warp = threadIdx.x >> 5, lane = lane_id(), q = warp & 3, half = (warp - kEpiWarp0) >> 2;
@@ -1290,15 +1322,15 @@ __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, 
     const int64_t och = static_cast<int64_t>(slab) * a.d + n;
     const float cs = a.terms && in ? __ldg(a.s_out + och) : 1.0f;
     const float bias = a.b_out != nullptr && in && first ? __ldg(a.b_out + och) : 0.0f;
-    const int acc = local & 1;
+    const int acc = local % kAccs, acc_n = tile_cols(p, c, 1, g), acc_col = cols_ring.take(acc_n);
     bool failed = false;
-    if (!mbar_wait(&c.tfull[acc], (local >> 1) & 1, &c.abort)) {
+    if (!mbar_wait(&c.tfull[acc], (local / kAccs) & 1, &c.abort)) {
       if (lane == 0) give_up(p, &c.abort);
       failed = true;
     }
     if (epi_any(failed)) return false;
     tc_fence_after();
-    const uint32_t tb = c.tmem_base + acc * kAccCols + half * (kAccCols / 2) + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t tb = c.tmem_base + acc_col + half * acc_n + (static_cast<uint32_t>(q * 32) << 16);
     // a whole tile's sums are the expert's outputs, a part's are added up at the end
     float* dst = whole ? p.outs + static_cast<int64_t>(row0) * a.d + n
                        : partial_of(p, f, blockIdx.x, u.tile * f.nk) + nl;
@@ -1374,6 +1406,7 @@ __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, cons
   const DecodeArgs& a = p.a;
   Ctl& c = *t.c;
   int local = 0;
+  AccRing cols;
   const bool inner_up = a.lora.n > 0 && (a.lora.a[0] != nullptr || a.lora.a[1] != nullptr);
   const bool inner_down = a.lora.n > 0 && a.lora.a[2] != nullptr;
   if (inner_up) {
@@ -1383,7 +1416,7 @@ __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, cons
     adapter_outer(p, t, 0, 2);
     epi_arrive(p, kOuterUp);
   }
-  if (!epilogue_up(p, t, up, local)) return;
+  if (!epilogue_up(p, t, up, local, cols)) return;
   epi_arrive(p, kHidden);
   if (a.terms || inner_down) {
     if (!epi_wait(p, kHidden, &c.abort)) return;
@@ -1405,7 +1438,7 @@ __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, cons
       epi_any(false);
     }
   }
-  if (!epilogue_down(p, t, down, local)) return;
+  if (!epilogue_down(p, t, down, local, cols)) return;
   epi_arrive(p, kSummed);
   if (!epi_wait(p, kSummed, &c.abort)) return;
   combine(p, t, down, reinterpret_cast<uchar2*>(ring));
@@ -1438,7 +1471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&c.full_b[i], 1);
         mbar_init(&c.empty[i], 1);
       }
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kAccs; ++i) {
         mbar_init(&c.tfull[i], 1);
         mbar_init(&c.tempty[i], kEpiThreads);
       }
