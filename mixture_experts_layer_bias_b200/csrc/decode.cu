@@ -774,15 +774,23 @@ __device__ void adapter_outer(const Params& p, const Tables& t, int m0, int nm) 
     }
     const float scale = __ldg(l.scale + ad);
     auto finish = [&](int c, const uint4 (&v)[8]) {
+      float s[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        float f[8], s = 0.0f;
+        float f[8];
         coding::bf16x8_to_f32(v[k], f);
+        s[k] = 0.0f;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) s = fmaf(f[q], uf[q], s);
-        for (int off = width >> 1; off >= 1; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+        for (int q = 0; q < 8; ++q) s[k] = fmaf(f[q], uf[q], s[k]);
+      }
+      for (int off = width >> 1; off >= 1; off >>= 1) {  // the eight sums' shuffles overlap
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], off);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
         const int col = c + k * per;
-        if (sub == 0 && col < c1) o[col] = s * scale;
+        if (sub == 0 && col < c1) o[col] = s[k] * scale;
       }
     };
     for (int c = b0 * batch + first; c - first < c1; c += 2 * batch) {
