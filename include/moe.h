@@ -411,10 +411,13 @@ moe_status moe_layer_forward_timed(const moe_desc *desc, const moe_weights *w, c
  * NULL or both given).  The expert outputs are summed in fp32 (no bf16
  * rounding per expert); the hidden rows are bf16 (two-term or W8A8 codes with
  * E4M3 weights), as in moe_grouped_ffn.  A capacity changes nothing (no row
- * is dropped).
+ * is dropped; MOE_CNT_OVERFLOW_ROWS is not counted).
  *   Supported: bf16 activations with bf16 weights (SwiGLU, GeLU) or E4M3
  *   weights (SwiGLU, act_quant 0 or 1, d and h multiples of 16), reroute = 0;
- *   MOE_ERR_UNSUPPORTED otherwise, MOE_ERR_INVALID_ARG for a larger S.
+ *   MOE_ERR_UNSUPPORTED otherwise, and for layers too large for the kernel's
+ *   tables (min(E, S * K) + num_shared experts of up to 20 M / that many
+ *   columns of d always fit, and 2^30 tiles of 128 x 64 weights);
+ *   MOE_ERR_INVALID_ARG for a larger S.
  *   ws: at least moe_decode_workspace_size bytes (lora may be NULL there),
  *   256-byte aligned, zeroed once by moe_workspace_init; its first 256 bytes
  *   hold the status block and the kernel's grid barrier, which every call

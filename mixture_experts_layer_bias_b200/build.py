@@ -7,9 +7,10 @@ next to this file so it ships with the package.  Only sources newer than their
 object are recompiled.
 
 A second library, libmoe_b200_testhooks.so, is linked from the same objects
-except the GEMM launch file, which is compiled with MOE_B200_TEST_HOOKS: it
-adds the failure-detection test hook (moe_test_stall_gemms) that the product
-library does not contain.  Only the failure-detection test loads it.
+except the GEMM launch file and the few-token layer, which are compiled with
+MOE_B200_TEST_HOOKS: it adds the failure-detection test hooks
+(moe_test_stall_gemms, moe_test_stall_decode) that the product library does not
+contain.  Only the failure-detection test loads it.
 
 A third, libmoe_b200_debug.so, is the guard build: the permutation and
 combine files are compiled with MOE_DEBUG, which adds a check kernel after
@@ -34,7 +35,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_b200.so")
 TEST_HOOKS_LIB = os.path.join(PKG, "libmoe_b200_testhooks.so")
-TEST_HOOKS_SOURCE = "gemm_dispatch.cu"
+TEST_HOOKS_SOURCES = ("gemm_dispatch.cu", "decode.cu")
 DEBUG_LIB = os.path.join(PKG, "libmoe_b200_debug.so")
 DEBUG_SOURCES = ("permute.cu", "combine.cu")
 
@@ -96,9 +97,9 @@ def build(force: bool = False, jobs: int = 8, extra=(), out: str = LIB, build_di
     if test_hooks and out == LIB:
         hook_dir = os.path.join(build_dir, "testhooks")
         os.makedirs(hook_dir, exist_ok=True)
-        hook_src = os.path.join(CSRC, TEST_HOOKS_SOURCE)
-        hook_obj = _compile(hook_src, force, list(extra) + ["-DMOE_B200_TEST_HOOKS"], hook_dir)
-        objs_h = [hook_obj if os.path.basename(o) == TEST_HOOKS_SOURCE + ".o" else o for o in objs]
+        hook = {src: _compile(os.path.join(CSRC, src), force, list(extra) + ["-DMOE_B200_TEST_HOOKS"], hook_dir)
+                for src in TEST_HOOKS_SOURCES}
+        objs_h = [hook.get(os.path.basename(o)[:-2], o) for o in objs]
         _link(objs_h, TEST_HOOKS_LIB, force)
         debug_dir = os.path.join(build_dir, "debug")
         os.makedirs(debug_dir, exist_ok=True)

@@ -316,7 +316,8 @@ LoraLayout lora_layout(const moe_desc& d, const moe_lora& l) {
 
 void lora_regions(const LoraLayout& L, void* ws, LoraCall* c) {
   char* base = static_cast<char*>(ws);
-  c->plan.counts = reinterpret_cast<int*>(base + L.counts);
+  c->plan.tile_count = reinterpret_cast<int*>(base + L.counts);
+  c->plan.rows = reinterpret_cast<unsigned long long*>(base + L.counts + 8);
   c->plan.tiles = reinterpret_cast<LoraTile*>(base + L.tiles);
   c->plan.list = reinterpret_cast<int2*>(base + L.list);
   c->plan.has = reinterpret_cast<uint8_t*>(base + L.has);
@@ -540,6 +541,7 @@ moe_status ffn_impl(const moe_desc& d, const moe_weights& w, const void* x_perm,
     a.token_of_row = lora->token_of_row;
     a.S = S;
     a.rows = Rt;
+    a.routed_rows = R;
     a.max_total_rows = up.max_total_rows;
     a.plan = lora->plan;
     a.counts_zeroed = lora->counts_zeroed;
@@ -633,7 +635,7 @@ moe_status layer_impl(const moe_desc* desc, const moe_weights* w, const void* x,
   if (!record(events, 0, st)) return MOE_ERR_CUDA;
   const int terms = a_terms(d);
   if (lora != nullptr) {
-    s = cuda_status(launch_route_exact(route_args(d, w, x, nullptr, idx, gates, ws), lora->wsq, lora->plan.counts, st));
+    s = cuda_status(launch_route_exact(route_args(d, w, x, nullptr, idx, gates, ws), lora->wsq, lora->plan.tile_count, st));
     lora->counts_zeroed = true;
   } else {
     s = route_impl(d, w, x, nullptr, idx, gates, ws, st);
@@ -674,6 +676,9 @@ moe_status decode_status(const moe_desc* desc) {
   if (desc->num_tokens > MOE_DECODE_MAX_TOKENS) return MOE_ERR_INVALID_ARG;
   if (desc->act_dtype != MOE_BF16 || desc->reroute != 0) return MOE_ERR_UNSUPPORTED;
   if (desc->weight_dtype == MOE_E4M3 && a_terms(*desc) == 0) return MOE_ERR_UNSUPPORTED;
+  if (!decode_supported(desc->num_tokens, desc->d_model, desc->num_experts, desc->top_k, desc->d_ff, desc->num_shared,
+                        a_terms(*desc)))
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

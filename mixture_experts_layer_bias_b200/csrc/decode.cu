@@ -159,6 +159,7 @@ struct Params {
   GridSync* sync;
   int stages, stage_bytes, ring_bytes;
   int stream_weights;  // weights leave L2 first
+  int test_stall;      // test hook: the producer delivers nothing (the bounded waits must give up)
 };
 
 // Shared-memory control block of one CTA; the selection's arrays follow it.
@@ -958,9 +959,10 @@ struct Producer {
   uint8_t* ring;
   Slot w, b;
   uint64_t hint;
-  uint32_t armed_w = 0, armed_b = 0, round_w = 0, round_b = 0;  // barriers armed, for an abort
+  uint32_t armed_w = 0, armed_b = 0, round_w = 0, round_b = 0;  // barriers armed, and their last rounds
 
-  __device__ Producer(const Params& p_, const Tables& t_, uint8_t* ring_) : p(p_), t(t_), ring(ring_) { hint = p.stream_weights ? l2_evict_first() : l2_evict_normal(); }
+  __device__ Producer(const Params& p_, const Tables& t_, uint8_t* ring_)
+      : p(p_), t(t_), ring(ring_), hint(p_.stream_weights ? l2_evict_first() : l2_evict_normal()) {}
 
   // Two weight tiles: rows n0 of slab `slab` of w0, and rows n1 of w1.
   __device__ bool weights(const CUtensorMap* w0, const CUtensorMap* w1, int k, int n0, int n1, int slab) {
@@ -1061,10 +1063,8 @@ __device__ void produce(const Params& p, const Tables& t, uint8_t* ring, const P
       }
     }
   }
-  if (!ok) {
-    if (lane_id() == 0) give_up(p, &c.abort);
-    pr.settle();
-  }
+  if (!ok && lane_id() == 0) give_up(p, &c.abort);
+  pr.settle();  // also where all went out: the MMA warp may give up before it has seen the last ones land
 }
 
 // TMEM columns of the units' accumulator pairs, one after another around the 512:
@@ -1231,12 +1231,11 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
       store_hidden(p, r, n, in, hidden_value(pair, rs, cs0, cs1, bias, v0, v1, d0, d1));
     };
     const int acc = local % kAccs, acc_n = tile_cols(p, c, 0, g), acc_col = cols_ring.take(acc_n);
-    bool failed = false;
-    if (!mbar_wait(&c.tfull[acc], (local / kAccs) & 1, &c.abort)) {
-      if (lane == 0) give_up(p, &c.abort);
-      failed = true;
+    const bool failed = !mbar_wait(&c.tfull[acc], (local / kAccs) & 1, &c.abort);
+    if (epi_any(failed)) {
+      if (threadIdx.x == 32 * kEpiWarp0) give_up(p, &c.abort);
+      return false;
     }
-    if (epi_any(failed)) return false;
     tc_fence_after();
     const uint32_t tb = c.tmem_base + acc_col + (static_cast<uint32_t>(q * 32) << 16);
     const uint64_t mask = c.mask[g];
@@ -1331,12 +1330,11 @@ __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, 
     const float cs = a.terms && in ? __ldg(a.s_out + och) : 1.0f;
     const float bias = a.b_out != nullptr && in && first ? __ldg(a.b_out + och) : 0.0f;
     const int acc = local % kAccs, acc_n = tile_cols(p, c, 1, g), acc_col = cols_ring.take(acc_n);
-    bool failed = false;
-    if (!mbar_wait(&c.tfull[acc], (local / kAccs) & 1, &c.abort)) {
-      if (lane == 0) give_up(p, &c.abort);
-      failed = true;
+    const bool failed = !mbar_wait(&c.tfull[acc], (local / kAccs) & 1, &c.abort);
+    if (epi_any(failed)) {
+      if (threadIdx.x == 32 * kEpiWarp0) give_up(p, &c.abort);
+      return false;
     }
-    if (epi_any(failed)) return false;
     tc_fence_after();
     const uint32_t tb = c.tmem_base + acc_col + half * acc_n + (static_cast<uint32_t>(q * 32) << 16);
     // a whole tile's sums are the expert's outputs, a part's are added up at the end
@@ -1505,7 +1503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     const Phase up = phase_of(c, 0, up_tiles_of(a), up_nk);
     const Phase down = phase_of(c, 1, (a.d + 255) / 256, down_nk);
-    if (warp == 0)
+    if (warp == 0 && !p.test_stall)
       produce(p, t, ring, up, down, &m_in0, pair ? &m_in1 : &m_in0, &m_out, &m_x, &m_hidden);
     else if (warp == 1 && lane_id() == 0)
       multiply(p, t, ring, up, down);
@@ -1527,6 +1525,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 size_t decode_workspace_bytes(int S, int d, int E, int K, int h, int num_shared, int terms, int lora_rank) {
   return ws_layout(S, d, E, K, h, num_shared, terms, lora_rank).total;
 }
+
+namespace {
+
+// Bytes of a stage: two weight tiles, then the columns of the largest possible group.
+int stage_bytes_of(int S, int terms) { return 2 * kTileBytes + ((S * (terms == 2 ? 2 : 1) + 15) & ~15) * 128; }
+
+int stages_of(int S, int K, int ns, int terms) {
+  const size_t room = kSmemLimit - 1024 - tables_bytes(S, K, ns);
+  return std::min<int>(kMaxStages, static_cast<int>(room / stage_bytes_of(S, terms)));
+}
+
+}  // namespace
+
+bool decode_supported(int S, int d, int E, int K, int h, int num_shared, int terms) {
+  if (S <= 0) return true;
+  const int stages = stages_of(S, K, num_shared, terms);
+  const int64_t ring = static_cast<int64_t>(stages) * stage_bytes_of(S, terms);
+  if (stages < 2 || ring < static_cast<int64_t>(sizeof(Scratch))) return false;
+  // steps and tiles are counted in 32 bits; the combine's table of tiles lies in the ring
+  const int64_t bk = terms ? 128 : 64, groups = std::min<int64_t>(E, static_cast<int64_t>(S) * K) + num_shared;
+  const int64_t up = groups * ((h + 127) / 128) * ((d + bk - 1) / bk), down = groups * ((d + 255) / 256) * ((h + bk - 1) / bk);
+  return up <= (1 << 30) && down <= (1 << 30) && 2 * groups * ((d + 255) / 256) <= ring;
+}
+
+#ifdef MOE_B200_TEST_HOOKS
+// Failure-detection test hook (the test build only): the next n launches run
+// with a producer that delivers nothing, so their waits give up.
+namespace {
+int g_stall_decode = 0;
+}
+extern "C" void moe_test_stall_decode(int n) { g_stall_decode = n > 0 ? n : 0; }
+#endif
 
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   static std::atomic<uint64_t> attr_set{0};  // one bit per device ordinal (host threads may launch concurrently)
@@ -1562,20 +1592,19 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   p.status = reinterpret_cast<StatusBlock*>(ws);
   p.sync = reinterpret_cast<GridSync*>(ws + kSyncOffset);
   const int terms = a.terms == 2 ? 2 : 1, eb = a.terms ? 1 : 2;
-  // a stage: two weight tiles, then the columns of the largest possible group
-  p.stage_bytes = 2 * kTileBytes + ((a.S * terms + 15) & ~15) * 128;
+  if (!decode_supported(a.S, a.d, a.E, a.K, a.h, a.num_shared, a.terms)) return cudaErrorInvalidValue;
   const size_t fixed = 1024 + tables_bytes(a.S, a.K, a.num_shared);
-  p.stages = static_cast<int>((kSmemLimit - fixed) / p.stage_bytes);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  if (p.stages < 2 || p.stages * p.stage_bytes < static_cast<int>(sizeof(Scratch))) return cudaErrorInvalidValue;
+  p.stage_bytes = stage_bytes_of(a.S, a.terms);
+  p.stages = stages_of(a.S, a.K, a.num_shared, a.terms);
   p.ring_bytes = p.stages * p.stage_bytes;
+  p.test_stall = 0;
+#ifdef MOE_B200_TEST_HOOKS
+  if (g_stall_decode > 0) {
+    --g_stall_decode;
+    p.test_stall = 1;
+  }
+#endif
   const int slabs = a.E + a.num_shared;
-  // steps are counted in 32 bits (two of them added at most)
-  const int64_t bk = a.terms ? 128 : 64;
-  if (slabs * ((a.h + 127) / 128) * ((a.d + bk - 1) / bk) > (1 << 30) ||
-      slabs * ((a.d + 255) / 256) * ((a.h + bk - 1) / bk) > (1 << 30))
-    return cudaErrorInvalidValue;
-  if (2 * slabs * ((a.d + 255) / 256) > p.ring_bytes) return cudaErrorInvalidValue;  // the combine's table of tiles
   const int64_t rows = static_cast<int64_t>(a.S) * (a.K + a.num_shared);
   CUtensorMap in0, in1, out, mx, mh;
   if (!gemm::make_slab_map(&in0, a.w_in[0], slabs, a.h, a.d, eb) || !gemm::make_slab_map(&out, a.w_out, slabs, a.d, a.h, eb))

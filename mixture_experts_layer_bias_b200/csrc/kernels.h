@@ -43,8 +43,7 @@ struct RouteArgs {
 };
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
 // The same selection for bf16 layers, decided by fp64 keys where fp32 ones are
-// too close to tell.  wsq: scratch [E]; zero (optional): two words set to zero on
-// the way.
+// too close to tell.  wsq: scratch [E]; zero: four words set to zero on the way.
 cudaError_t launch_route_exact(const RouteArgs& a, float* wsq, int* zero, cudaStream_t stream);
 // x W_r^T alone, into logits_scratch.
 cudaError_t launch_router_logits(const RouteArgs& a, cudaStream_t stream);
@@ -205,7 +204,8 @@ struct LoraTile {
   int expert, adapter, pos, rows;  // its inner products: rows pos .. pos + rows - 1 of u
 };
 struct LoraPlan {
-  int* counts;         // [2]: tiles, listed rows
+  int* tile_count;           // its 16 bytes are zero before the plan kernel: the tiles made,
+  unsigned long long* rows;  // ... and, 8 bytes on, the rows listed
   LoraTile* tiles;     // [max_total_rows]
   int2* list;          // [32 max_total_rows]: tile i's rows from 32 i on: (row of the row space, token)
   uint8_t* has;        // [rows]: 1 where the row's token has an adapter (rows of the groups only)
@@ -217,9 +217,10 @@ struct LoraPlanArgs {
   const int32_t* token_of_row;
   int S;
   int64_t rows;            // rows of the row space
-  int64_t max_total_rows;  // bound of the rows of all groups together
+  int64_t routed_rows;     // ... of those, without the shared expert's: rows of token_of_row and of x_perm
+  int64_t max_total_rows;  // bound of the rows of all groups together: the lists' room
   LoraPlan plan;
-  int counts_zeroed;       // 1: an earlier kernel of the call has set counts to zero
+  int counts_zeroed;       // 1: an earlier kernel of the call has set the counts to zero
   StatusBlock* status;
 };
 cudaError_t launch_lora_plan(const LoraPlanArgs& a, cudaStream_t stream);
@@ -273,6 +274,8 @@ struct DecodeArgs {
 };
 // Workspace bytes of launch_decode for this shape (lora_rank 0: no adapters).
 size_t decode_workspace_bytes(int S, int d, int E, int K, int h, int num_shared, int terms, int lora_rank);
+// Whether the kernel's shared-memory tables and 32-bit counts hold this shape.
+bool decode_supported(int S, int d, int E, int K, int h, int num_shared, int terms);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 
 // --- combine -----------------------------------------------------------------

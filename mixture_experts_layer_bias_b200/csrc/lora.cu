@@ -65,15 +65,25 @@ __device__ int block_prefix(int v, int* warp_sums, int* total) {
 __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const LoraPlanArgs a) {
   __shared__ int hist[kLoraMaxAdapters];  // rows of each adapter, then its next entry
   __shared__ int warp_sums[kPlanThreads / 32];
-  __shared__ int base_tile, base_row;
+  __shared__ int base_tile, base_row, refused;
   pdl_wait();
   pdl_trigger();
   const GroupEntry ge = a.groups[blockIdx.x];
-  const bool ok = ge.rows > 0 && ge.rows <= a.S && ge.expert >= 0 && ge.expert < a.slabs && ge.out_row0 >= 0 &&
+  const bool ok = ge.rows > 0 && ge.expert >= 0 && ge.expert < a.slabs && ge.out_row0 >= 0 &&
                   static_cast<int64_t>(ge.out_row0) + ge.rows <= a.rows;
-  if (!ok) return;  // the GEMM reports it
+  if (!ok) return;  // empty, or the GEMM skips it and says so
   const int tid = threadIdx.x, n = a.lora.n;
   const bool shared = ge.expert == a.shared_slab;
+  // Group tables made from a caller's offsets may overlap: whoever claims rows that
+  // x_perm, token_of_row or the lists do not have is left without adapters.
+  auto refuse = [&]() {
+    if (tid == 0) report(a.status, MOE_STATUS_BAD_GROUP, -1);
+    for (int i = tid; i < ge.rows; i += kPlanThreads) a.plan.has[ge.out_row0 + i] = 0;
+  };
+  if (ge.rows > a.S || (!shared && static_cast<int64_t>(ge.out_row0) + ge.rows > a.routed_rows)) {
+    refuse();
+    return;
+  }
   for (int i = tid; i < n; i += kPlanThreads) hist[i] = 0;
   __syncthreads();
   auto adapter_of = [&](int i, int& token) {
@@ -102,10 +112,16 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const LoraPlanA
   int row = block_prefix(rows, warp_sums, &all_rows);
   int tile = block_prefix(tiles, warp_sums, &all_tiles);
   if (tid == 0) {
-    base_tile = all_tiles > 0 ? atomicAdd(&a.plan.counts[0], all_tiles) : 0;
-    base_row = all_rows > 0 ? atomicAdd(&a.plan.counts[1], all_rows) : 0;
+    const unsigned long long at = all_rows > 0 ? atomicAdd(a.plan.rows, static_cast<unsigned long long>(all_rows)) : 0;
+    refused = at + all_rows > static_cast<unsigned long long>(a.max_total_rows);
+    base_row = static_cast<int>(at);
+    base_tile = all_tiles > 0 && !refused ? atomicAdd(a.plan.tile_count, all_tiles) : 0;
   }
   __syncthreads();
+  if (refused) {
+    refuse();
+    return;
+  }
   row += base_row;
   tile += base_tile;
   for (int i = a0; i < a1; ++i) {
@@ -168,7 +184,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lora_inner_kernel(const LoraRo
   const int block = warp % nb, kslice = warp / nb;
   pdl_wait();
   pdl_trigger();
-  const int units = a.plan.counts[0] * sh.splits;
+  const int units = *a.plan.tile_count * sh.splits;
   if (blockIdx.x < units) meta_store(meta[0], meta_load(a.plan, blockIdx.x / sh.splits));
   __syncthreads();
   for (int un = blockIdx.x, buf = 0; un < units; un += gridDim.x, buf ^= 1) {
@@ -317,7 +333,7 @@ __global__ void __launch_bounds__(kOuterThreads, KSTEPS <= 2 ? 6 : 4) lora_outer
   const int blocks = (a.N + block - 1) / block;
   pdl_wait();
   pdl_trigger();
-  const int units = a.plan.counts[0] * blocks;
+  const int units = *a.plan.tile_count * blocks;
   if (blockIdx.x < units) meta_store(meta[0], meta_load(a.plan, blockIdx.x / blocks));
   __syncthreads();
   for (int un = blockIdx.x, buf = 0; un < units; un += gridDim.x, buf ^= 1) {
@@ -426,7 +442,7 @@ cudaError_t launch_lora_plan(const LoraPlanArgs& a, cudaStream_t stream) {
   if (a.num_groups <= 0 || a.num_groups > gemm::kMaxGroups || a.lora.n > kLoraMaxAdapters) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   if (!a.counts_zeroed) {
-    if ((e = cudaMemsetAsync(a.plan.counts, 0, 2 * sizeof(int), stream)) != cudaSuccess) return e;
+    if ((e = cudaMemsetAsync(a.plan.tile_count, 0, 16, stream)) != cudaSuccess) return e;
     lora_plan_kernel<<<a.num_groups, kPlanThreads, 0, stream>>>(a);  // (behind a memset: no dependent launch)
   } else {
     e = launch_pdl(lora_plan_kernel, dim3(a.num_groups), dim3(kPlanThreads), 0, stream, a);

@@ -201,13 +201,13 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Squared lengths of the router's rows, a warp per row; `zero` (optional): two
+// Squared lengths of the router's rows, a warp per row; `zero`: four
 // words that a later kernel of the call counts in.
 __global__ void __launch_bounds__(128) router_norm_kernel(const __nv_bfloat16* w, int E, int d, float* wsq, int* zero) {
   const int e = blockIdx.x * 4 + (threadIdx.x >> 5);
   pdl_wait();
   pdl_trigger();
-  if (zero != nullptr && blockIdx.x == 0 && threadIdx.x < 2) zero[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && threadIdx.x < 4) zero[threadIdx.x] = 0;
   if (e >= E) return;
   float sq = 0.0f;
 #pragma unroll 4
@@ -372,7 +372,7 @@ __device__ bool select_fast(const ExactParams& p, int tok, const float* approx, 
       warp_argmax(bv, bg);
       if (round == p.topk_groups) {
         // sums of gs keys, with the roundings of their own additions
-        if (last - bv <= 4.0f * gs * err) return false;
+        if (!(last - bv > 4.0f * gs * err)) return false;  // (a bound that overflowed decides nothing either)
         break;
       }
       last = bv;
@@ -398,7 +398,7 @@ __device__ bool select_fast(const ExactParams& p, int tok, const float* approx, 
     }
     warp_argmax(bv, be);
     if (be >= p.E) break;  // fewer than K + 1 candidates
-    if (k > 0 && last - bv <= 2.0f * err) return false;
+    if (k > 0 && !(last - bv > 2.0f * err)) return false;
     last = bv;
     float sc = 0.0f;
 #pragma unroll
@@ -452,8 +452,8 @@ __device__ __noinline__ void select_token(const ExactParams& p, int tok, const f
     group_limit<NI>(p, key, cand, &gap);
     const double slope = p.score_fn == MOE_SCORE_SIGMOID ? 0.25 : 1.0 / static_cast<double>(p.tau);
     const double tol = slope * static_cast<double>(err);
-    if (gap <= 2.0 * tol * (p.E / p.num_groups)) {
-      // which groups are kept is open: every expert's exact logit
+    if (!(gap > 2.0 * tol * (p.E / p.num_groups)) || !isfinite(tol)) {
+      // which groups are kept is open, or the bound overflowed: every expert's exact logit
       for (int e0 = 0; e0 < p.E; e0 += 2) {
         const int n = min(2, p.E - e0);
         const int e[2] = {e0, min(e0 + 1, p.E - 1)};

@@ -72,6 +72,18 @@ def test_decode_takes_few_tokens_of_bf16_layers():
     assert _size_code(_desc(top_k=9)) == ops.MOE_ERR_INVALID_ARG
 
 
+def test_decode_refuses_layers_its_tables_cannot_hold():
+    # 256 experts' tiles of 256 columns at two bytes a tile have to fit beside the weight ring's shared memory
+    big = dict(num_tokens=64, num_experts=256, top_k=8, d_ff=512)
+    assert _size_code(_desc(d_model=79872, **big)) == ops.MOE_OK
+    assert _size_code(_desc(d_model=131072, **big)) == ops.MOE_ERR_UNSUPPORTED
+    assert _size_code(_desc(d_model=131072, **dict(big, num_tokens=1))) == ops.MOE_OK  # 8 experts at most
+    # more than 2^30 steps
+    assert _size_code(_desc(num_tokens=1, num_experts=8, top_k=8, d_model=1 << 20, d_ff=1 << 21)) == ops.MOE_ERR_UNSUPPORTED
+    d, w = _desc(d_model=131072, **big), _weights()
+    assert _decode(d, w, None, None, n=1 << 40) == ops.MOE_ERR_UNSUPPORTED
+
+
 def test_decode_workspace_grows_with_the_batch_and_the_rank():
     one, all_ = (ops.moe_decode_workspace_size(_desc(num_tokens=S)) for S in (1, 64))
     assert one % 256 == 0 and all_ > one

@@ -226,6 +226,64 @@ def test_adapters_match_float64(cfg, n, rank, pairs):
     assert rows_rel(np64(y)[keep], ref[keep]) <= 1.5 * tol(k)
 
 
+EDGES = [
+    (_c(BASE, S=3, d=8, h=8), 2, 8, None), (_c(E4, S=5, d=16, h=16), 2, 8, None),
+    (_c(BASE, S=64, E=2, K=2), 1, 128, None),             # every token: the same adapter, the same experts
+    (_c(BASE, S=64, E=1, K=1, num_shared=1), 64, 128, None),
+    (_c(GELU, S=17, num_shared=1), 3, 16, ("down",)), (_c(GELU, S=17, num_shared=1), 3, 16, ("up",)),
+    (_c(E4, S=17, num_shared=1), 3, 16, ("gate", "down")), (_c(BASE, S=31, E=64, K=32, d=256, h=128), 4096, 8, ("up",)),
+]
+
+
+@pytest.mark.parametrize("cfg,n,rank,pairs", EDGES, ids=[f"{_id(c)}-n{n}-r{r}-{p or 'all'}" for c, n, r, p in EDGES])
+def test_adapters_at_the_edges_of_their_range(cfg, n, rank, pairs):
+    inp = syn.make_inputs(cfg, "cuda", seed=14)
+    ad = make_adapters(cfg, n, rank, seed=3, pairs=pairs or ("gate", "up", "down"))
+    ids = make_ids(cfg.S, n, seed=4) if n > 1 else torch.zeros(cfg.S, dtype=torch.int32, device="cuda")
+    ids[0] = n - 1
+    layer, y = _run(cfg, inp, ad, ids)
+    assert layer.status()[1] == 0
+    ref, idx, _, margin = reference_layer(inp, cfg, ad, ids)
+    keep = margin >= MARGIN
+    assert (layer.topk_idx.cpu().numpy()[keep] == idx[keep]).all()
+    # as above; over a handful of elements a rounding need not be better than half a step, sqrt(3) times its root mean square
+    k = 4 if cfg.weight_dtype == syn.E4M3 else 2
+    assert rel_l2(np64(y)[keep], ref[keep]) <= tol(k) * (3 ** 0.5 if cfg.d < 64 else 1)
+
+
+@pytest.mark.parametrize("cfg", [_c(BASE, S=1, d=1024, h=2048), _c(E4, S=33), _c(FINE, S=40)], ids=_id)
+def test_adapters_repeat_bit_identically_and_replay_on_another_stream(cfg):
+    inp = syn.make_inputs(cfg, "cuda", seed=15)
+    ad = make_adapters(cfg, 5, 16)
+    ids = make_ids(cfg.S, 5)
+    layer = MoELayer(cfg, inp, adapters=ad)
+    first = layer.decode(inp["x"], adapter_ids=ids).clone()
+    graphs = []
+    for _ in range(2):
+        y = torch.empty_like(first)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer.decode(inp["x"], y=y, adapter_ids=ids)
+        graphs.append((g, y))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            for g, y in graphs:
+                y.zero_()
+                g.replay()
+            assert torch.equal(layer.decode(inp["x"], adapter_ids=ids), first)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, first) for _, y in graphs)
+    # other adapters in the captured buffer
+    ids.copy_((ids + 2) % 5)
+    graphs[0][0].replay()
+    torch.cuda.synchronize()
+    other = graphs[0][1].clone()
+    assert torch.equal(layer.decode(inp["x"], adapter_ids=ids), other) and not torch.equal(other, first)
+    assert layer.status()[1] == 0
+
+
 def test_tokens_without_adapter_and_bad_ids():
     cfg = _c(BASE, S=20)
     inp = syn.make_inputs(cfg, "cuda", seed=12)

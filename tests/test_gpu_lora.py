@@ -139,6 +139,73 @@ def test_stage_call_equals_the_layer(base):
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("base,offsets", [
+    (BASE, [0, 64, 0, 64, 0, 64, 0, 64, 0]),                     # four groups claim all rows: twice the lists' room
+    (_c(BASE, num_shared=1), [0, 8, 16, 24, 32, 40, 48, 118, 138]),  # the last one runs into the shared expert's rows
+    (_c(BASE, capacity=64), list(range(0, 513, 64)) + [0] * 9),   # every expert full: more rows than S * K
+], ids=("overlap", "past-the-routed-rows", "full"))
+def test_offsets_that_claim_too_many_rows_leave_groups_without_adapters(base, offsets):
+    """Groups whose rows the adapters' lists have no room for go without adapters and are reported."""
+    cfg = _c(base, S=64)
+    inp = syn.make_inputs(cfg, "cuda", seed=26)
+    layer = MoELayer(cfg, inp, adapters=make_adapters(cfg, 4, 16))
+    R = ops.moe_routed_rows(layer.desc)
+    assert max(offsets) <= R + cfg.num_shared * 64
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    tor = (torch.arange(R, dtype=torch.int32) % 64).cuda()
+    ids = torch.arange(64, dtype=torch.int32, device="cuda") % 4
+    xp = torch.zeros((R, cfg.d), dtype=torch.bfloat16, device="cuda")
+    xp[:] = inp["x"][tor.long()]
+    yp = torch.full((R + cfg.num_shared * 64 + 1, cfg.d), 7.0, dtype=torch.bfloat16, device="cuda")
+    ops.moe_grouped_ffn_lora(layer.desc, layer.weights, layer.lora, ids, xp, off, tor, inp["x"], yp, layer.ws)
+    torch.cuda.synchronize()
+    assert layer.status()[1] & ops.MOE_STATUS_BAD_GROUP
+    assert (yp[-1] == 7.0).all()
+    # a good call on the same workspace
+    ops.moe_workspace_init(layer.ws)
+    ref = MoELayer(cfg, inp, adapters=make_adapters(cfg, 4, 16))
+    assert torch.equal(layer.forward(inp["x"], adapter_ids=ids), ref.forward(inp["x"], adapter_ids=ids))
+    assert layer.status()[1] == 0
+
+
+def test_calls_on_two_streams_at_once():
+    cfg = _c(BASE, S=200, num_shared=1)
+    inp = syn.make_inputs(cfg, "cuda", seed=27)
+    ad, ids = make_adapters(cfg, 6, 24), runs(200, 6)
+    want = MoELayer(cfg, inp, adapters=ad).forward(inp["x"], adapter_ids=ids).clone()
+    layers = [MoELayer(cfg, inp, adapters=ad) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for layer, st in zip(layers, streams):
+            layer.forward(inp["x"], stream=st, adapter_ids=ids)
+    torch.cuda.synchronize()
+    for layer in layers:
+        assert torch.equal(layer.y, want) and layer.status()[1] == 0
+
+
+@pytest.mark.parametrize("cfg,n,rank", [
+    (_c(BASE, S=200, E=2, K=2), 1, 128), (_c(BASE, S=90, d=8, h=8), 3, 8), (_c(BASE, S=150, E=64, K=32, d=256, h=128), 4096, 8),
+    (_c(E4, S=77, d=16, h=16), 2, 8), (_c(E4, S=130, E=1, K=1, num_shared=1), 130, 128),
+], ids=("one-adapter", "narrow", "most-adapters", "narrow-e4m3", "an-adapter-each"))
+def test_adapters_at_the_edges_of_their_range(cfg, n, rank):
+    inp = syn.make_inputs(cfg, "cuda", seed=28)
+    ad = make_adapters(cfg, n, rank, seed=3, pairs=("up", "down") if n < 4096 else ("up",))
+    ids = (torch.arange(cfg.S, dtype=torch.int32) % n).cuda()
+    ids[0] = n - 1
+    layer = MoELayer(cfg, inp, adapters=ad)
+    y = layer.forward(inp["x"], adapter_ids=ids)
+    torch.cuda.synchronize()
+    assert layer.status()[1] == 0
+    ref, idx, _, margin = reference_layer(inp, cfg, ad, ids)
+    keep = margin >= MARGIN
+    assert (layer.topk_idx.cpu().numpy()[keep] == idx[keep]).all()
+    # roundings: hidden rows, expert outputs, y, the inner products and the deltas of the two stages (each of a part of
+    # the sum), the codes; over narrow rows a rounding need not be better than half a step
+    k = 9 if cfg.weight_dtype == syn.E4M3 else 7
+    assert rel_l2(np64(y)[keep], ref[keep]) <= tol(k) * (3 ** 0.5 if cfg.d < 64 else 1)
+
+
 def test_decode_and_prefill_of_the_same_requests():
     """As a server uses them: a prompt batch through forward, then the same
     requests' next tokens through decode, one set of adapters."""
