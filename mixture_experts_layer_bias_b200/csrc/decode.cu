@@ -175,6 +175,7 @@ struct Ctl {
   int abort;
   int active;
   int last;
+  int others_done[2];  // of a cut up tile's parts: all but this CTA's (by the unit's parity)
   int warp_sums[kWarps];
   int warp_costs[kWarps];
   int first[kMaxSlabs + 1];            // active group -> its first row
@@ -373,7 +374,7 @@ __device__ __forceinline__ uint64_t ordered(double v) {
 
 // Tokens that a CTA selects at once: a thread per (token, expert).
 __device__ __forceinline__ int select_width(int E) {
-  int w = 32;
+  int w = 8;
   while (w < E) w <<= 1;
   return w;
 }
@@ -1149,55 +1150,56 @@ __device__ void multiply(const Params& p, const Tables& t, uint8_t* ring, const 
   if (!ok) give_up(p, &c.abort);
 }
 
-// Eight accumulator columns -> the sums of their 8 (or, two terms, 4) tokens.
-__device__ __forceinline__ void load_sums(uint32_t taddr, int terms, float (&v)[8]) {
+// Eight accumulator columns -> the sums of their tokens: 8, or 4 of two terms each.
+template <int TERMS>
+__device__ __forceinline__ void load_sums(uint32_t taddr, float (&v)[TERMS == 2 ? 4 : 8]) {
   uint32_t r[8];
   tmem_ld_32x32b_x8(taddr, r);
   tmem_ld_wait();
+  if (TERMS == 2) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-  if (terms == 2) {
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[2 * i]) + __uint_as_float(r[2 * i + 1]);
+  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = v[2 * i] + v[2 * i + 1];
+    for (int i = 0; i < (TERMS == 2 ? 4 : 8); ++i) v[i] = __uint_as_float(r[i]);
   }
 }
 
 // Hidden value from a row's final sums v0, v1 (gate and up, or v0 alone): the
 // row's scale rs and the column's cs0, cs1 (1 without E4M3 weights), the
-// adapters' share d0, d1, bias, activation.
-__device__ __forceinline__ float hidden_value(bool pair, float rs, float cs0, float cs1, float bias, float v0, float v1,
-                                              float d0, float d1) {
+// adapters' share d0, d1, bias, activation.  The quick division (off by two units
+// in the last place; 0 where the sigmoid is below 2^-126) has no branches, so the
+// rows of a chunk overlap.
+template <bool PAIR>
+__device__ __forceinline__ float hidden_value(float rs, float cs0, float cs1, float bias, float v0, float v1, float d0,
+                                              float d1) {
   v0 = fmaf(v0, rs * cs0, d0);
-  if (pair) {
+  if (PAIR) {
     v1 = fmaf(v1, rs * cs1, d1);
-    return v0 / (1.0f + __expf(-v0)) * v1;
+    return __fdividef(v0, 1.0f + __expf(-v0)) * v1;
   }
   const float z = v0 + bias;
   return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
 }
 
-// Store hidden value `v` of (row, n) and, with E4M3 weights, raise the row's
-// maximum (one atomic per warp; lanes past the last column pass in = false).
-__device__ __forceinline__ void store_hidden(const Params& p, int r, int n, bool in, float v) {
-  const __nv_bfloat16 q = __float2bfloat16_rn(v);
-  if (in) p.hidden[static_cast<int64_t>(r) * p.a.h + n] = q;
-  if (p.a.terms) {
-    const uint32_t bits = in ? (__bfloat16_as_ushort(q) & 0x7FFFu) : 0u;
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, bits);
-    if (lane_id() == 0) atomicMax(p.amax + r, m);
-  }
-}
-
 // One hidden element of a tile: tile column `n` (0..127) of half `m`.
 __device__ __forceinline__ int hidden_col(bool pair, int j, int m, int n) { return pair ? j * 128 + n : j * 256 + m * 128 + n; }
 
+// Hidden rows of a CTA's tiles.  The 8 columns that a warp reads from its
+// accumulators at once are the chunk of rows that it finishes at once: every step
+// runs over the whole chunk before the next one, because two warps per scheduler
+// hide little of one row's chain of instructions.  A cut tile's parts meet in the
+// CTA that comes last: mostly it finds the others' parts complete when it starts on
+// its own and adds them to the sums in its registers; else all parts go through
+// memory.  Either way they are added in CTA order.
+template <bool PAIR, int TERMS>
 __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, int& local, AccRing& cols_ring) {
   const DecodeArgs& a = p.a;
   Ctl& c = *t.c;
+  constexpr int kPer = TERMS == 2 ? 4 : 8;  // rows of a chunk
   const int warp = threadIdx.x >> 5, lane = lane_id(), q = warp & 3, half = (warp - kEpiWarp0) >> 2;
-  const bool pair = a.activation == MOE_ACT_SWIGLU, dense = all_tokens(a.S, a.terms);
+  const bool dense = all_tokens(a.S, TERMS);
   const int tiles = up_tiles_of(a);
-  const int terms = a.terms == 2 ? 2 : 1, per = 8 / terms;  // tokens per 8 columns
   const int nl = q * 32 + lane;
   const bool outer = a.lora.n > 0 && (a.lora.a[0] != nullptr || a.lora.a[1] != nullptr);
   bool outer_ready = !outer;
@@ -1208,111 +1210,162 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
     const int row0 = c.first[g], cnt = c.first[g + 1] - row0;
     const bool whole = u.k0 == 0 && u.k1 == f.nk;
     const int s0 = u.tile * f.nk;
+    const int c0 = whole ? 0 : f.part_of(s0), c1 = whole ? 0 : f.last_part(c0, s0 + f.nk - 1);
     float* part = partial_of(p, f, blockIdx.x, s0);
     if (!outer_ready) {
       if (!epi_wait(p, kOuterUp, &c.abort)) return false;
       outer_ready = true;
     }
-    const int n = hidden_col(pair, j, half, nl);
+    const int n = hidden_col(PAIR, j, half, nl);
     const bool in = n < a.h;
     float cs0 = 1.0f, cs1 = 1.0f, bias = 0.0f;  // the column's scales or bias, loaded while the sums are made
     if (in) {
       const int64_t ch = static_cast<int64_t>(slab) * a.h + n;
-      if (a.terms) {
+      if (TERMS) {
         cs0 = __ldg(a.s_in[0] + ch);
         cs1 = __ldg(a.s_in[1] + ch);
       }
-      if (!pair) bias = __ldg(a.b_in + ch);
+      if (!PAIR) bias = __ldg(a.b_in + ch);
     }
-    auto adapted = [&](int r) { return outer && in && c.adapter[t.row_tok[r]] >= 0; };
-    auto share = [&](int r, int m) { return __ldcg(p.d_in + (static_cast<int64_t>(r) * 2 + m) * a.h + n); };
-    auto finish = [&](int r, float v0, float v1, float d0, float d1) {
-      const float rs = a.terms ? t.row_scale[r] : 1.0f;
-      store_hidden(p, r, n, in, hidden_value(pair, rs, cs0, cs1, bias, v0, v1, d0, d1));
-    };
     const int acc = local % kAccs, acc_n = tile_cols(p, c, 0, g), acc_col = cols_ring.take(acc_n);
+    int& all_there = c.others_done[local & 1];  // (two: a slow warp may still look at the unit before)
+    if (threadIdx.x == 32 * kEpiWarp0)
+      all_there = !whole && ld_acquire(p.joins + c0) == static_cast<uint32_t>(c1 - c0);
     const bool failed = !mbar_wait(&c.tfull[acc], (local / kAccs) & 1, &c.abort);
     if (epi_any(failed)) {
       if (threadIdx.x == 32 * kEpiWarp0) give_up(p, &c.abort);
       return false;
     }
     tc_fence_after();
+    const bool complete = whole || all_there;
     const uint32_t tb = c.tmem_base + acc_col + (static_cast<uint32_t>(q * 32) << 16);
     const uint64_t mask = c.mask[g];
     const int cols = dense ? a.S : cnt;  // tokens in the tile's columns
-    // SwiGLU: the two halves of the warps take alternate chunks of columns, both tiles; else one tile each
-    for (int ch = pair ? half : 0; ch * per < cols; ch += pair ? 2 : 1) {
-      float v0[8], v1[8], d0[8], d1[8];
-      auto row_of = [&](int col) {  // the row of column col (-1: none)
-        if (col >= cols) return -1;
-        if (!dense) return row0 + col;
-        return (mask >> col) & 1 ? row0 + __popcll(mask & ((uint64_t(1) << col) - 1)) : -1;
-      };
+    // the adapters' share of the rows r, and their hidden values from complete sums
+    auto shares = [&](const int (&r)[kPer], float (&d0)[kPer], float (&d1)[kPer]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kPer; ++i) {
         d0[i] = d1[i] = 0.0f;
-        const int r = i < per ? row_of(ch * per + i) : -1;
-        if (whole && r >= 0 && adapted(r)) {
-          d0[i] = share(r, pair ? 0 : 1);
-          if (pair) d1[i] = share(r, 1);
+        if (outer && in && r[i] >= 0 && c.adapter[t.row_tok[r[i]]] >= 0) {
+          const float* d = p.d_in + static_cast<int64_t>(r[i]) * 2 * a.h + n;
+          d0[i] = __ldcg(d + (PAIR ? 0 : a.h));
+          if (PAIR) d1[i] = __ldcg(d + a.h);
         }
       }
-      load_sums(tb + (pair ? 0 : half * acc_n) + ch * 8, terms, v0);
-      if (pair) load_sums(tb + acc_n + ch * 8, terms, v1);
+    };
+    auto finish = [&](const int (&r)[kPer], const float (&v0)[kPer], const float (&v1)[kPer], const float (&d0)[kPer],
+                      const float (&d1)[kPer]) {
+      __nv_bfloat16 hv[kPer];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = i < per ? row_of(ch * per + i) : -1;
-        if (r < 0) continue;
-        if (!whole) {
-          float* o = part + (r - row0) * 256 + nl;
-          o[pair ? 0 : half * 128] = v0[i];
-          if (pair) o[128] = v1[i];
-          continue;
+      for (int i = 0; i < kPer; ++i)
+        hv[i] = __float2bfloat16_rn(hidden_value<PAIR>(TERMS && r[i] >= 0 ? t.row_scale[r[i]] : 1.0f, cs0, cs1, bias,
+                                                       v0[i], PAIR ? v1[i] : 0.0f, d0[i], d1[i]));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (in && r[i] >= 0) p.hidden[static_cast<int64_t>(r[i]) * a.h + n] = hv[i];
+      if (TERMS) {  // the rows' maxima: lane i raises that of row r[i]
+        uint32_t top = 0;
+        int at = -1;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, in ? __bfloat16_as_ushort(hv[i]) & 0x7FFFu : 0u);
+          if (lane == i) {
+            top = m;
+            at = r[i];
+          }
         }
-        finish(r, v0[i], pair ? v1[i] : 0.0f, d0[i], d1[i]);
+        if (at >= 0) atomicMax(p.amax + at, top);
       }
+    };
+    // SwiGLU: the two halves of the warps take alternate chunks of columns, both tiles; else one tile each
+    for (int ch = PAIR ? half : 0; ch * kPer < cols; ch += PAIR ? 2 : 1) {
+      float v0[kPer], v1[kPer], d0[kPer], d1[kPer];
+      int r[kPer];  // the columns' rows (-1: none)
+      uint32_t some = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int col = ch * kPer + i;
+        r[i] = col < cols ? row0 + col : -1;
+        if (dense) r[i] = col < cols && ((mask >> col) & 1) ? row0 + __popcll(mask & ((uint64_t(1) << col) - 1)) : -1;
+        some |= r[i] >= 0;
+      }
+      if (!some) continue;
+      if (complete) shares(r, d0, d1);
+      load_sums<TERMS>(tb + (PAIR ? 0 : half * acc_n) + ch * 8, v0);
+      if (PAIR) load_sums<TERMS>(tb + acc_n + ch * 8, v1);
+      if (!complete) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (r[i] < 0) continue;
+          float* o = part + (r[i] - row0) * 256 + nl;
+          o[PAIR ? 0 : half * 128] = v0[i];
+          if (PAIR) o[128] = v1[i];
+        }
+        continue;
+      }
+      if (!whole) {
+        float s0v[kPer], s1v[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) s0v[i] = s1v[i] = 0.0f;
+        for (int cc = c0; cc <= c1; ++cc) {
+          if (cc == static_cast<int>(blockIdx.x)) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+              s0v[i] += v0[i];
+              if (PAIR) s1v[i] += v1[i];
+            }
+            continue;
+          }
+          const float* src = partial_of(p, f, cc, s0) + nl + (PAIR ? 0 : half * 128);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            if (r[i] < 0) continue;
+            s0v[i] += __ldcg(src + (r[i] - row0) * 256);
+            if (PAIR) s1v[i] += __ldcg(src + (r[i] - row0) * 256 + 128);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          v0[i] = s0v[i];
+          if (PAIR) v1[i] = s1v[i];
+        }
+      }
+      finish(r, v0, v1, d0, d1);
     }
     tc_fence_before();
     mbar_arrive(&c.tempty[acc]);
-    if (whole) continue;
-    const int c0 = f.part_of(s0), c1 = f.last_part(c0, s0 + f.nk - 1);
-    if (!join_last(p, t, c0, c1)) continue;
-    // rows four at a time, so that their loads are in flight together
-    const int step = pair ? 8 : 4;
-    for (int i0 = pair ? half * 4 : 0; i0 < cnt; i0 += step) {
-      float v0[4] = {0.f, 0.f, 0.f, 0.f}, v1[4] = {0.f, 0.f, 0.f, 0.f};
-      float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+    if (complete || !join_last(p, t, c0, c1)) continue;
+    const int step = PAIR ? 2 * kPer : kPer;
+    for (int i0 = PAIR ? half * kPer : 0; i0 < cnt; i0 += step) {
+      float v0[kPer], v1[kPer], d0[kPer], d1[kPer];
+      int r[kPer];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = row0 + i0 + i;
-        if (i0 + i < cnt && adapted(r)) {
-          d0[i] = share(r, pair ? 0 : 1);
-          if (pair) d1[i] = share(r, 1);
-        }
+      for (int i = 0; i < kPer; ++i) {
+        r[i] = i0 + i < cnt ? row0 + i0 + i : -1;
+        v0[i] = v1[i] = 0.0f;
       }
+      shares(r, d0, d1);
       for (int cc = c0; cc <= c1; ++cc) {
-        const float* src = partial_of(p, f, cc, s0) + i0 * 256 + nl + (pair ? 0 : half * 128);
+        const float* src = partial_of(p, f, cc, s0) + i0 * 256 + nl + (PAIR ? 0 : half * 128);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i0 + i < cnt) {
-            v0[i] += __ldcg(src + i * 256);
-            if (pair) v1[i] += __ldcg(src + i * 256 + 128);
-          }
+        for (int i = 0; i < kPer; ++i) {
+          if (r[i] < 0) continue;
+          v0[i] += __ldcg(src + i * 256);
+          if (PAIR) v1[i] += __ldcg(src + i * 256 + 128);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i0 + i < cnt) finish(row0 + i0 + i, v0[i], v1[i], d0[i], d1[i]);
+      finish(r, v0, v1, d0, d1);
     }
   }
   return true;
 }
 
+template <int TERMS>
 __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, int& local, AccRing& cols_ring) {
   const DecodeArgs& a = p.a;
   Ctl& c = *t.c;
   const int warp = threadIdx.x >> 5, lane = lane_id(), q = warp & 3, half = (warp - kEpiWarp0) >> 2;
-  const int terms = a.terms == 2 ? 2 : 1, per = 8 / terms;
+  constexpr int kPer = TERMS == 2 ? 4 : 8;    // rows of a chunk
   const int nl = half * 128 + q * 32 + lane;  // this thread's column of the tile
   const bool outer = a.lora.n > 0 && a.lora.a[2] != nullptr;
   bool outer_ready = !outer;
@@ -1327,7 +1380,7 @@ __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, 
       outer_ready = true;
     }
     const int64_t och = static_cast<int64_t>(slab) * a.d + n;
-    const float cs = a.terms && in ? __ldg(a.s_out + och) : 1.0f;
+    const float cs = TERMS && in ? __ldg(a.s_out + och) : 1.0f;
     const float bias = a.b_out != nullptr && in && first ? __ldg(a.b_out + och) : 0.0f;
     const int acc = local % kAccs, acc_n = tile_cols(p, c, 1, g), acc_col = cols_ring.take(acc_n);
     const bool failed = !mbar_wait(&c.tfull[acc], (local / kAccs) & 1, &c.abort);
@@ -1341,22 +1394,20 @@ __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, 
     float* dst = whole ? p.outs + static_cast<int64_t>(row0) * a.d + n
                        : partial_of(p, f, blockIdx.x, u.tile * f.nk) + nl;
     const int64_t stride = whole ? a.d : 256;
-    for (int ch = 0; ch * per < cnt; ++ch) {
-      float v[8], dd[8];
+    for (int ch = 0; ch * kPer < cnt; ++ch) {
+      float v[kPer], dd[kPer];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int tk = ch * per + i;
+      for (int i = 0; i < kPer; ++i) {
+        const int tk = ch * kPer + i;
         dd[i] = bias;
-        if (i < per && tk < cnt && outer && first && in && c.adapter[t.row_tok[row0 + tk]] >= 0)
+        if (tk < cnt && outer && first && in && c.adapter[t.row_tok[row0 + tk]] >= 0)
           dd[i] += __ldcg(p.d_out + static_cast<int64_t>(row0 + tk) * a.d + n);
       }
-      load_sums(tb + ch * 8, terms, v);
+      load_sums<TERMS>(tb + ch * 8, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int tk = ch * per + i;
-        if (i >= per || tk >= cnt) break;
-        const float rs = a.terms ? t.row_scale[row0 + tk] : 1.0f;
-        if (in) dst[tk * stride] = fmaf(v[i], rs * cs, dd[i]);
+      for (int i = 0; i < kPer; ++i) {
+        const int tk = ch * kPer + i;
+        if (tk < cnt && in) dst[tk * stride] = TERMS ? fmaf(v[i], t.row_scale[row0 + tk] * cs, dd[i]) : v[i] + dd[i];
       }
     }
     tc_fence_before();
@@ -1408,6 +1459,7 @@ __device__ void combine(const Params& p, const Tables& t, const Phase& f, uchar2
   }
 }
 
+template <bool PAIR, int TERMS>
 __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, const Phase& down, uint8_t* ring) {
   const DecodeArgs& a = p.a;
   Ctl& c = *t.c;
@@ -1422,11 +1474,11 @@ __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, cons
     adapter_outer(p, t, 0, 2);
     epi_arrive(p, kOuterUp);
   }
-  if (!epilogue_up(p, t, up, local, cols)) return;
+  if (!epilogue_up<PAIR, TERMS>(p, t, up, local, cols)) return;
   epi_arrive(p, kHidden);
-  if (a.terms || inner_down) {
+  if (TERMS || inner_down) {
     if (!epi_wait(p, kHidden, &c.abort)) return;
-    if (a.terms) {
+    if (TERMS) {
       code_hidden(p, t);
       epi_arrive(p, kCoded);
     }
@@ -1437,14 +1489,14 @@ __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, cons
       adapter_outer(p, t, 2, 1);
       epi_arrive(p, kOuterDown);
     }
-    if (a.terms) {  // the hidden rows' scales
+    if (TERMS) {  // the hidden rows' scales
       if (!epi_wait(p, kCoded, &c.abort)) return;
       for (int r = threadIdx.x - 32 * kEpiWarp0; r < c.first[c.active]; r += kEpiThreads)
         t.row_scale[r] = __ldcg(p.hs + r);
       epi_any(false);
     }
   }
-  if (!epilogue_down(p, t, down, local, cols)) return;
+  if (!epilogue_down<TERMS>(p, t, down, local, cols)) return;
   epi_arrive(p, kSummed);
   if (!epi_wait(p, kSummed, &c.abort)) return;
   combine(p, t, down, reinterpret_cast<uchar2*>(ring));
@@ -1507,8 +1559,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       produce(p, t, ring, up, down, &m_in0, pair ? &m_in1 : &m_in0, &m_out, &m_x, &m_hidden);
     else if (warp == 1 && lane_id() == 0)
       multiply(p, t, ring, up, down);
+    else if (warp >= kEpiWarp0 && a.terms == 2)
+      epilogue<true, 2>(p, t, up, down, ring);
+    else if (warp >= kEpiWarp0 && a.terms == 1)
+      epilogue<true, 1>(p, t, up, down, ring);
+    else if (warp >= kEpiWarp0 && pair)
+      epilogue<true, 0>(p, t, up, down, ring);
     else if (warp >= kEpiWarp0)
-      epilogue(p, t, up, down, ring);
+      epilogue<false, 0>(p, t, up, down, ring);
     __syncwarp();
   }
   tc_fence_before();
