@@ -187,6 +187,7 @@ struct Ctl {
   uint64_t mask[kMaxSlabs];            // active group -> its tokens
   uint64_t tokens_of[kMaxSlabs];       // slab -> its tokens
   int adapter[MOE_DECODE_MAX_TOKENS];  // token -> adapter or -1
+  float scale[MOE_DECODE_MAX_TOKENS];  // E4M3: token -> its codes' scale
 };
 
 // Scratch of the routing, in the ring before its first copy.
@@ -502,6 +503,10 @@ __device__ bool tables_phase(const Params& p, const Tables& t) {
   const int slots = a.S * a.K, slabs = a.E + a.num_shared;
   const int width = select_width(a.E), per = kThreads / width, rounds = (a.S + per - 1) / per;
   for (int i = tid; i < slabs; i += kThreads) c.tokens_of[i] = 0;
+  // a token's adapter and its codes' scale, loaded while the selection runs
+  const bool adapted = a.lora.n > 0 && tid < a.S;
+  const int id = adapted ? __ldg(a.lora.ids + tid) : -1;
+  const float scale = a.terms && tid < a.S ? __ldcg(p.xs + tid) : 1.0f;
   if (rounds <= 2) {
     for (int r = 0; r < rounds; ++r)
       select_tokens(p, sc, r * per, min(per, a.S - r * per), width, sc.idx, sc.gate, blockIdx.x == 0);
@@ -517,17 +522,13 @@ __device__ bool tables_phase(const Params& p, const Tables& t) {
   }
   // an expert's tokens as a 64-bit mask: its rows are the set bits in token order
   for (int i = tid; i < slots; i += kThreads)
-    atomicOr(reinterpret_cast<unsigned long long*>(c.tokens_of + sc.idx[i]), 1ull << (i / a.K));
-  if (tid == 0 && a.num_shared) c.tokens_of[a.E] = a.S == 64 ? ~uint64_t(0) : (uint64_t(1) << a.S) - 1;
-  if (a.lora.n > 0) {
-    for (int i = tid; i < a.S; i += kThreads) {
-      int id = __ldg(a.lora.ids + i);
-      if (id < -1 || id >= a.lora.n) {
-        if (blockIdx.x == 0) report(p.status, MOE_STATUS_BAD_ADAPTER, -1);
-        id = -1;
-      }
-      c.adapter[i] = id;
-    }
+    atomicOr(reinterpret_cast<uint32_t*>(c.tokens_of + sc.idx[i]) + (i / a.K >> 5), 1u << (i / a.K & 31));
+  if (tid == kThreads - 1 && a.num_shared) c.tokens_of[a.E] = a.S == 64 ? ~uint64_t(0) : (uint64_t(1) << a.S) - 1;
+  if (tid < a.S) {
+    const bool known = id >= -1 && id < a.lora.n;
+    if (adapted && !known && blockIdx.x == 0) report(p.status, MOE_STATUS_BAD_ADAPTER, -1);
+    c.adapter[tid] = adapted && known ? id : -1;
+    c.scale[tid] = scale;
   }
   __syncthreads();
   // exclusive prefix over the slabs of (rows, active groups)
@@ -582,7 +583,7 @@ __device__ bool tables_phase(const Params& p, const Tables& t) {
     t.row_grp[r] = static_cast<uint16_t>(c.group[e]);
     t.row_gate[r] = shared ? 1.0f : sc.gate[i];
     if (!shared) t.slot_row[i] = static_cast<uint16_t>(r);
-    if (a.terms) t.row_scale[r] = __ldcg(p.xs + tok);
+    if (a.terms) t.row_scale[r] = c.scale[tok];
   }
   if (blockIdx.x == 0) {
     if (a.counts != nullptr && tid < a.E) a.counts[tid] = count;
@@ -857,12 +858,12 @@ struct Phase {
   }
 };
 
-// All threads: the ranges of a phase of `tiles` tiles per group, tile after tile
-// within a group (up), or group after group within a tile (down).
+// Half of the threads: the ranges of a phase of `tiles` tiles per group, tile after
+// tile within a group (up), or group after group within a tile (down).
 __device__ void cut_phase(Ctl& c, int ph, int tiles, int nk, bool equal) {
   const int total = c.active * tiles * nk, parts = min(total, static_cast<int>(gridDim.x));
   const int weight = c.weight[c.active];
-  for (int i = threadIdx.x; i <= parts; i += kThreads) {
+  for (int i = threadIdx.x % (kThreads / 2); i <= parts; i += kThreads / 2) {
     int s;
     if (equal || total < 4 * parts || i == parts) {
       // equal costs, or too few steps to weigh them (a range must not be empty): equal numbers, the longer ones first
@@ -1277,6 +1278,43 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
         if (at >= 0) atomicMax(p.amax + at, top);
       }
     };
+    // v0, v1 become the sums over the parts c0 .. c1 in that order, this CTA's own from v0, v1 (own) or from memory as
+    // well; kBatch parts' loads are in flight together
+    auto add_parts = [&](const int (&r)[kPer], bool own, float (&v0)[kPer], float (&v1)[kPer]) {
+      constexpr int kBatch = PAIR && TERMS != 2 ? 2 : 4;
+      float sum0[kPer], sum1[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sum0[i] = sum1[i] = 0.0f;
+      for (int cc = c0; cc <= c1; cc += kBatch) {
+        float q0[kBatch][kPer], q1[kBatch][kPer];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const bool mine = own && cc + b == static_cast<int>(blockIdx.x), load = cc + b <= c1 && !mine;
+          const float* src = partial_of(p, f, min(cc + b, c1), s0) + nl + (PAIR ? 0 : half * 128);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            q0[b][i] = mine ? v0[i] : 0.0f;
+            if (load && r[i] >= 0) q0[b][i] = __ldcg(src + (r[i] - row0) * 256);
+            if (PAIR) {
+              q1[b][i] = mine ? v1[i] : 0.0f;
+              if (load && r[i] >= 0) q1[b][i] = __ldcg(src + (r[i] - row0) * 256 + 128);
+            }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            sum0[i] += q0[b][i];
+            if (PAIR) sum1[i] += q1[b][i];
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        v0[i] = sum0[i];
+        if (PAIR) v1[i] = sum1[i];
+      }
+    };
     // SwiGLU: the two halves of the warps take alternate chunks of columns, both tiles; else one tile each
     for (int ch = PAIR ? half : 0; ch * kPer < cols; ch += PAIR ? 2 : 1) {
       float v0[kPer], v1[kPer], d0[kPer], d1[kPer];
@@ -1303,33 +1341,7 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
         }
         continue;
       }
-      if (!whole) {
-        float s0v[kPer], s1v[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) s0v[i] = s1v[i] = 0.0f;
-        for (int cc = c0; cc <= c1; ++cc) {
-          if (cc == static_cast<int>(blockIdx.x)) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-              s0v[i] += v0[i];
-              if (PAIR) s1v[i] += v1[i];
-            }
-            continue;
-          }
-          const float* src = partial_of(p, f, cc, s0) + nl + (PAIR ? 0 : half * 128);
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            if (r[i] < 0) continue;
-            s0v[i] += __ldcg(src + (r[i] - row0) * 256);
-            if (PAIR) s1v[i] += __ldcg(src + (r[i] - row0) * 256 + 128);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          v0[i] = s0v[i];
-          if (PAIR) v1[i] = s1v[i];
-        }
-      }
+      if (!whole) add_parts(r, true, v0, v1);
       finish(r, v0, v1, d0, d1);
     }
     tc_fence_before();
@@ -1342,18 +1354,10 @@ __device__ bool epilogue_up(const Params& p, const Tables& t, const Phase& f, in
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         r[i] = i0 + i < cnt ? row0 + i0 + i : -1;
-        v0[i] = v1[i] = 0.0f;
+        v0[i] = v1[i] = 0.0f;  // (this CTA's part comes from memory too)
       }
       shares(r, d0, d1);
-      for (int cc = c0; cc <= c1; ++cc) {
-        const float* src = partial_of(p, f, cc, s0) + i0 * 256 + nl + (PAIR ? 0 : half * 128);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          if (r[i] < 0) continue;
-          v0[i] += __ldcg(src + i * 256);
-          if (PAIR) v1[i] += __ldcg(src + i * 256 + 128);
-        }
-      }
+      add_parts(r, false, v0, v1);
       finish(r, v0, v1, d0, d1);
     }
   }
@@ -1416,19 +1420,22 @@ __device__ bool epilogue_down(const Params& p, const Tables& t, const Phase& f, 
   return true;
 }
 
-// y[t] = sum_k gate_k * expert output of its k-th row (+ the shared expert's), four
-// columns per thread of the grid: whole tiles' outputs, or the parts of a cut tile
-// in CTA order.  parts (shared memory, the idle ring): each tile's first CTA, and
-// how many more hold parts of it.
-__device__ void combine(const Params& p, const Tables& t, const Phase& f, uchar2* parts) {
-  const DecodeArgs& a = p.a;
-  const Ctl& c = *t.c;
-  const int quads = a.d / 4, slots = a.S * a.K, tid = threadIdx.x - 32 * kEpiWarp0;
-  for (int i = tid; i < f.total / f.nk; i += kEpiThreads) {
+// Each down tile's first CTA and how many more hold parts of it, into shared memory
+// (the ring, idle once this CTA's own products are done).
+__device__ void list_parts(const Phase& f, uchar2* parts) {
+  for (int i = threadIdx.x - 32 * kEpiWarp0; i < f.total / f.nk; i += kEpiThreads) {
     const int c0 = f.part_of(i * f.nk);
     parts[i] = make_uchar2(c0, f.last_part(c0, i * f.nk + f.nk - 1) - c0);
   }
-  epi_any(false);
+}
+
+// y[t] = sum_k gate_k * expert output of its k-th row (+ the shared expert's), four
+// columns per thread of the grid: whole tiles' outputs, or the parts of a cut tile
+// in CTA order, four parts' loads in flight together.
+__device__ void combine(const Params& p, const Tables& t, const Phase& f, const uchar2* parts) {
+  const DecodeArgs& a = p.a;
+  const Ctl& c = *t.c;
+  const int quads = a.d / 4, slots = a.S * a.K, tid = threadIdx.x - 32 * kEpiWarp0;
   auto* y = static_cast<__nv_bfloat16*>(a.y);
   for (int i = blockIdx.x * kEpiThreads + tid; i < a.S * quads; i += gridDim.x * kEpiThreads) {
     const int tk = i / quads, n = (i - tk * quads) * 4, j = n / 256;
@@ -1442,12 +1449,21 @@ __device__ void combine(const Params& p, const Tables& t, const Phase& f, uchar2
       const int64_t at = static_cast<int64_t>(r - c.first[g]) * 256 + n % 256;
       const float* src = pt.y == 0 ? p.outs + static_cast<int64_t>(r) * a.d + n : partial_of(p, f, pt.x, tile * f.nk) + at;
       float4 o = __ldcg(reinterpret_cast<const float4*>(src));
-      for (int cc = 1; cc <= pt.y; ++cc) {
-        const float4 q = __ldcg(reinterpret_cast<const float4*>(partial_of(p, f, pt.x + cc, tile * f.nk) + at));
-        o.x += q.x;
-        o.y += q.y;
-        o.z += q.z;
-        o.w += q.w;
+      for (int cc = 1; cc <= pt.y; cc += 4) {
+        float4 q[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          q[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (cc + b <= pt.y)
+            q[b] = __ldcg(reinterpret_cast<const float4*>(partial_of(p, f, pt.x + cc + b, tile * f.nk) + at));
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          o.x += q[b].x;
+          o.y += q[b].y;
+          o.z += q[b].z;
+          o.w += q[b].w;
+        }
       }
       v.x = fmaf(gate, o.x, v.x);
       v.y = fmaf(gate, o.y, v.y);
@@ -1498,8 +1514,10 @@ __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, cons
   }
   if (!epilogue_down<TERMS>(p, t, down, local, cols)) return;
   epi_arrive(p, kSummed);
-  if (!epi_wait(p, kSummed, &c.abort)) return;
-  combine(p, t, down, reinterpret_cast<uchar2*>(ring));
+  auto* parts = reinterpret_cast<uchar2*>(ring);
+  list_parts(down, parts);
+  if (!epi_wait(p, kSummed, &c.abort)) return;  // (its barrier also closes the table)
+  combine(p, t, down, parts);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -1550,8 +1568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int bk = a.terms ? 128 : 64;
     const int up_nk = (a.d + bk - 1) / bk, down_nk = (a.h + bk - 1) / bk;
     const bool equal = all_tokens(a.S, a.terms);
-    cut_phase(c, 0, up_tiles_of(a), up_nk, equal);
-    cut_phase(c, 1, (a.d + 255) / 256, down_nk, equal);
+    const int ph = threadIdx.x >= kThreads / 2;
+    cut_phase(c, ph, ph == 0 ? up_tiles_of(a) : (a.d + 255) / 256, ph == 0 ? up_nk : down_nk, equal);
     __syncthreads();
     const Phase up = phase_of(c, 0, up_tiles_of(a), up_nk);
     const Phase down = phase_of(c, 1, (a.d + 255) / 256, down_nk);
