@@ -76,7 +76,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kEpiWarp0 = 4;  // epilogue warps 4 .. 11
 constexpr int kEpiThreads = kThreads - 32 * kEpiWarp0;
 constexpr int kMaxSlabs = 257;
-constexpr int kRouteTokens = 8;  // tokens per warp of the logits
+constexpr int kRouteTokens = 8;  // tokens per item of the logits
 constexpr int kMaxStages = 8;
 constexpr int kMaxSlices = 8;  // of K, in the adapters' inner products
 constexpr int kTileBytes = 128 * 128;  // one weight tile of a step: 128 rows x 128 bytes of K
@@ -305,9 +305,10 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Router logits, a CTA per (expert, 8 tokens), the threads striding over d in
-// 16-byte pieces: a bf16 product is exact in fp32 and is summed in fp64.  With
-// E4M3 weights also the tokens' codes, a warp per token, by the CTAs from the
+// Router logits, a team of a CTA's warps per (expert, 8 tokens), striding over d in
+// 16-byte pieces: a bf16 product is exact in fp32 and is summed in fp64.  (64 tokens
+// and 64 experts: 124 us for the layer with teams of 3 warps in one round, 128 with
+// the whole CTA in four.)  With E4M3 weights also the tokens' codes, a warp per token, by the CTAs from the
 // other end of the grid.  The join counters and row maxima start at zero.
 __device__ void route_phase(const Params& p, Scratch& c) {
   const DecodeArgs& a = p.a;
@@ -324,14 +325,18 @@ __device__ void route_phase(const Params& p, Scratch& c) {
                            p.xs + t, a.d, a.terms, lane);
   }
   const int items = a.E * ((a.S + kRouteTokens - 1) / kRouteTokens);
-  for (int i = blockIdx.x; i < items; i += gridDim.x) {
-    const int e = i % a.E, t0 = (i / a.E) * kRouteTokens, nt = min(kRouteTokens, a.S - t0);
+  int team = kWarps;  // warps of an item: as many as leave one round of items
+  while (team > 1 && items > static_cast<int>(gridDim.x) * (kWarps / team)) team = kWarps / (kWarps / team + 1);
+  const int teams = kWarps / team, mine = warp / team, rank = (warp - mine * team) * 32 + lane;
+  for (int i0 = blockIdx.x * teams; i0 < items; i0 += gridDim.x * teams) {
+    const int i = i0 + mine;
+    const int e = i % a.E, t0 = (i / a.E) * kRouteTokens, nt = i < items ? min(kRouteTokens, a.S - t0) : 0;
     const auto* w = static_cast<const __nv_bfloat16*>(a.w_router) + static_cast<int64_t>(e) * a.d;
     const auto* xt = x + static_cast<int64_t>(t0) * a.d;
     double acc[kRouteTokens];
 #pragma unroll
     for (int j = 0; j < kRouteTokens; ++j) acc[j] = 0.0;
-    for (int k = tid * 8; k < a.d; k += kThreads * 8) {
+    for (int k = rank * 8; k < a.d && nt > 0; k += team * 256) {
       float wf[8];
       uint4 xv[kRouteTokens];
       const uint4 wv = ldg16(w + k);
@@ -358,10 +363,10 @@ __device__ void route_phase(const Params& p, Scratch& c) {
       }
     }
     __syncthreads();
-    if (tid < nt) {
+    if (rank < nt) {
       double v = a.router_bias != nullptr ? static_cast<double>(__ldg(a.router_bias + e)) : 0.0;
-      for (int k = 0; k < kWarps; ++k) v += c.sum[k * kRouteTokens + tid];
-      p.logits[static_cast<int64_t>(t0 + tid) * a.E + e] = v;
+      for (int k = 0; k < team; ++k) v += c.sum[(mine * team + k) * kRouteTokens + rank];
+      p.logits[static_cast<int64_t>(t0 + rank) * a.E + e] = v;
     }
     __syncthreads();
   }
