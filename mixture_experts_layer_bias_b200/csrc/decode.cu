@@ -6,7 +6,7 @@
 // With a handful of tokens the layer is bound by reading the touched experts'
 // weights once, and a chain of kernels leaves HBM idle at every boundary.
 // Here the steps are phases of one grid:
-//   route    logits in fp64, a CTA per (expert, 8 tokens); with E4M3 weights
+//   route    logits in fp64, a few warps per (expert, 8 tokens); with E4M3 weights
 //            also the tokens' row codes; then the selection and the expert
 //            groups, which every CTA builds in its own shared memory
 //   up       hidden = act(x W_in)
@@ -26,7 +26,7 @@
 // tile, k) for up and (tile, group, k) for down, are cut into one range of
 // equal cost per CTA (see step_cost), whatever the group sizes are.  A tile
 // cut by a range border goes through fp32 partial sums in the workspace: in the
-// up phase whichever of its CTAs arrives last joins them, in the down phase the
+// up phase whichever of its CTAs comes last adds them up, in the down phase the
 // whole grid adds them at the end, together with the gate-weighted sum over a
 // token's experts.  Both add in CTA order, so results do not depend on timing.
 //
@@ -37,7 +37,8 @@
 // held the up phase at 4.8 TB/s for one token.)
 //
 // Roles (384 threads): warp 0 feeds a ring of stages by TMA, warp 1 issues the
-// MMAs, warps 4 - 11 are the epilogue, two per TMEM lane quarter.  The weights of
+// MMAs, warps 4 - 11 are the epilogue, two per TMEM lane quarter (2 and 3 help it
+// with the adapters).  The weights of
 // the down phase do not depend on the hidden rows, so the producer fills the
 // whole ring with them while the up phase drains and the grid waits for the last
 // hidden row.
@@ -48,8 +49,8 @@
 // not matter) while the up phase stores the bf16 hidden rows, and the epilogue
 // warps write the codes between the phases.
 //
-// Adapters: while the tensor cores start on a phase, the epilogue warps of the
-// whole grid take the inner products u = A x (up) or A hidden (down) and then the
+// Adapters: while the tensor cores start on a phase, warps 2 - 11 of the whole grid
+// take the inner products u = A x (up) or A hidden (down) and then the
 // outer ones scale * B u, in equal shares, into fp32 buffers; the epilogue adds
 // those to a tile's final sums.  (Made by the epilogue itself, tile by tile, the
 // outer products kept the CTAs of the busiest expert 150 us longer than the others.)
@@ -75,6 +76,8 @@ constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 constexpr int kEpiWarp0 = 4;  // epilogue warps 4 .. 11
 constexpr int kEpiThreads = kThreads - 32 * kEpiWarp0;
+constexpr int kLoraWarp0 = 2;  // warps 2 .. 11 take the adapters' products
+constexpr int kLoraWarps = kWarps - kLoraWarp0;
 constexpr int kMaxSlabs = 257;
 constexpr int kRouteTokens = 8;  // tokens per item of the logits
 constexpr int kMaxStages = 8;
@@ -237,40 +240,45 @@ __device__ __forceinline__ void give_up(const Params& p, volatile int* abort_fla
   report(p.status, MOE_STATUS_TIMEOUT, MOE_CNT_TIMEOUT);
 }
 
-// The epilogue warps' barrier; true when any of them passes `failed`.  Its
-// answer is the same for all, so they leave a loop together or not at all.
-__device__ __forceinline__ bool epi_any(bool failed) {
+// A barrier (`id`) of the warps from WARP0 on; true when any of them passes
+// `failed`.  Its answer is the same for all, so they leave a loop together or not
+// at all.
+template <int WARP0>
+__device__ __forceinline__ bool any_of(bool failed) {
   int any;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.s32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+      "barrier.cta.red.or.pred q, %3, %2, p;\n\t"
       "selp.s32 %0, 1, 0, q;\n\t}"
       : "=r"(any)
-      : "r"(static_cast<int>(failed)), "n"(kEpiThreads)
+      : "r"(static_cast<int>(failed)), "n"(kThreads - 32 * WARP0), "n"(WARP0 == kEpiWarp0 ? 1 : 2)
       : "memory");
   return any != 0;
 }
+__device__ __forceinline__ bool epi_any(bool failed) { return any_of<kEpiWarp0>(failed); }
 
-// The epilogue warps arrive at `k` for their CTA once their writes are done
+// The warps from WARP0 on arrive at `k` for their CTA once their writes are done
 // (written by the generic proxy, read by other CTAs through either).
+template <int WARP0 = kEpiWarp0>
 __device__ __forceinline__ void epi_arrive(const Params& p, Arrival k) {
   fence_proxy_async_global();
-  epi_any(false);
-  if (threadIdx.x == 32 * kEpiWarp0) {
+  any_of<WARP0>(false);
+  if (threadIdx.x == 32 * WARP0) {
     __threadfence();  // (the barrier before it makes this cover every warp's writes)
     atomicAdd(&p.sync->arrived[k], 1);
   }
 }
 
-// The epilogue warps wait for `k`; false (for all of them) when it gave up.
+// They wait for `k`; false (for all of them) when it gave up.
+template <int WARP0 = kEpiWarp0>
 __device__ __forceinline__ bool epi_wait(const Params& p, Arrival k, volatile int* abort_flag) {
   bool failed = false;
-  if (threadIdx.x == 32 * kEpiWarp0 && !wait_arrivals(p, k, abort_flag)) {
+  if (threadIdx.x == 32 * WARP0 && !wait_arrivals(p, k, abort_flag)) {
     give_up(p, abort_flag);
     failed = true;
   }
-  return !epi_any(failed);
+  return !any_of<WARP0>(failed);
 }
 
 // Every thread of every CTA: false when the wait gave up.
@@ -620,9 +628,9 @@ __device__ bool tables_phase(const Params& p, const Tables& t) {
   return grid_barrier(p, c, kPacked);
 }
 
-// This warp's share [lo, hi) of n items that the grid's epilogue warps divide.
+// This warp's share [lo, hi) of n items that the grid's warps 2 .. 11 divide.
 __device__ __forceinline__ void warp_share(int n, int& lo, int& hi) {
-  const int warps = gridDim.x * (kEpiThreads / 32), w = ((threadIdx.x >> 5) - kEpiWarp0) * gridDim.x + blockIdx.x;
+  const int warps = gridDim.x * kLoraWarps, w = ((threadIdx.x >> 5) - kLoraWarp0) * gridDim.x + blockIdx.x;
   const int q = n / warps, r = n - q * warps;
   lo = w * q + min(w, r);
   hi = lo + q + (w < r ? 1 : 0);
@@ -630,11 +638,11 @@ __device__ __forceinline__ void warp_share(int n, int& lo, int& hi) {
 
 // Slices of K of the inner products: about two items for every warp of the grid.
 __device__ __forceinline__ int inner_slices(int items, int pieces) {
-  const int warps = gridDim.x * (kEpiThreads / 32);
+  const int warps = gridDim.x * kLoraWarps;
   return max(1, min(min(kMaxSlices, pieces), 2 * warps / max(items, 1)));
 }
 
-// Epilogue warps: u[slice][row][m][i] = A_m[a][slab][i] . row over a slice of K, for
+// Warps 2 .. 11: u[slice][row][m][i] = A_m[a][slab][i] . row over a slice of K, for
 // the pairs m0 .. m0 + nm - 1.  An item is (row, pair, 8 values, slice): the row's
 // pieces of 256 meet eight rows of A, nine loads per lane and piece; a warp
 // streams through its items' pieces with the next one's loads always under way.
@@ -724,7 +732,7 @@ __device__ void adapter_inner(const Params& p, const Tables& t, int m0, int nm) 
   }
 }
 
-// Epilogue warps: out[row][m][n] = scale * sum_i u[row][m][i] B_m[a][slab][n][i].
+// Warps 2 .. 11: out[row][m][n] = scale * sum_i u[row][m][i] B_m[a][slab][n][i].
 // r / 8 neighbouring lanes (rounded up to a power of two) take 16 bytes each of a
 // column's row of B and add up by shuffles; eight loads per lane make a batch of
 // columns, the next batch's under way, and a warp takes an equal run of batches.
@@ -1480,6 +1488,19 @@ __device__ void combine(const Params& p, const Tables& t, const Phase& f, const 
   }
 }
 
+// Warps 2 .. 11: the adapters' share of a phase; false when a wait gave up.  (33
+// tokens with 32 adapters of rank 64 over fine E4M3 experts: 233 us; 242 with the
+// epilogue's eight warps alone, or with one copy of this code that is called.)
+__device__ __forceinline__ bool adapter_products(const Params& p, const Tables& t, int m0, int nm, Arrival inner, Arrival outer) {
+  adapter_inner(p, t, m0, nm);
+  epi_arrive<kLoraWarp0>(p, inner);
+  if (!epi_wait<kLoraWarp0>(p, inner, &t.c->abort)) return false;
+  adapter_outer(p, t, m0, nm);
+  epi_arrive<kLoraWarp0>(p, outer);
+  return true;
+}
+
+// Warps 4 .. 11; with adapters also warps 2 and 3, which help with their products.
 template <bool PAIR, int TERMS>
 __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, const Phase& down, uint8_t* ring) {
   const DecodeArgs& a = p.a;
@@ -1488,34 +1509,26 @@ __device__ void epilogue(const Params& p, const Tables& t, const Phase& up, cons
   AccRing cols;
   const bool inner_up = a.lora.n > 0 && (a.lora.a[0] != nullptr || a.lora.a[1] != nullptr);
   const bool inner_down = a.lora.n > 0 && a.lora.a[2] != nullptr;
-  if (inner_up) {
-    adapter_inner(p, t, 0, 2);
-    epi_arrive(p, kInnerUp);
-    if (!epi_wait(p, kInnerUp, &c.abort)) return;
-    adapter_outer(p, t, 0, 2);
-    epi_arrive(p, kOuterUp);
+  const bool helper = threadIdx.x < 32 * kEpiWarp0;
+  if (inner_up && !adapter_products(p, t, 0, 2, kInnerUp, kOuterUp)) return;
+  bool ok = true;
+  if (!helper) {
+    ok = epilogue_up<PAIR, TERMS>(p, t, up, local, cols);
+    if (ok) epi_arrive(p, kHidden);
+    if (ok && (TERMS || inner_down)) ok = epi_wait(p, kHidden, &c.abort);
   }
-  if (!epilogue_up<PAIR, TERMS>(p, t, up, local, cols)) return;
-  epi_arrive(p, kHidden);
-  if (TERMS || inner_down) {
-    if (!epi_wait(p, kHidden, &c.abort)) return;
-    if (TERMS) {
-      code_hidden(p, t);
-      epi_arrive(p, kCoded);
-    }
-    if (inner_down) {
-      adapter_inner(p, t, 2, 1);
-      epi_arrive(p, kInnerDown);
-      if (!epi_wait(p, kInnerDown, &c.abort)) return;
-      adapter_outer(p, t, 2, 1);
-      epi_arrive(p, kOuterDown);
-    }
-    if (TERMS) {  // the hidden rows' scales
-      if (!epi_wait(p, kCoded, &c.abort)) return;
-      for (int r = threadIdx.x - 32 * kEpiWarp0; r < c.first[c.active]; r += kEpiThreads)
-        t.row_scale[r] = __ldcg(p.hs + r);
-      epi_any(false);
-    }
+  // (the helpers wait here for the hidden rows, and learn it if there will be none)
+  if (inner_down ? any_of<kLoraWarp0>(!ok) : !ok) return;
+  if (!helper && TERMS) {
+    code_hidden(p, t);
+    epi_arrive(p, kCoded);
+  }
+  if (inner_down && !adapter_products(p, t, 2, 1, kInnerDown, kOuterDown)) return;
+  if (helper) return;
+  if (TERMS) {  // the hidden rows' scales
+    if (!epi_wait(p, kCoded, &c.abort)) return;
+    for (int r = threadIdx.x - 32 * kEpiWarp0; r < c.first[c.active]; r += kEpiThreads) t.row_scale[r] = __ldcg(p.hs + r);
+    epi_any(false);
   }
   if (!epilogue_down<TERMS>(p, t, down, local, cols)) return;
   epi_arrive(p, kSummed);
@@ -1582,14 +1595,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       produce(p, t, ring, up, down, &m_in0, pair ? &m_in1 : &m_in0, &m_out, &m_x, &m_hidden);
     else if (warp == 1 && lane_id() == 0)
       multiply(p, t, ring, up, down);
-    else if (warp >= kEpiWarp0 && a.terms == 2)
-      epilogue<true, 2>(p, t, up, down, ring);
-    else if (warp >= kEpiWarp0 && a.terms == 1)
-      epilogue<true, 1>(p, t, up, down, ring);
-    else if (warp >= kEpiWarp0 && pair)
-      epilogue<true, 0>(p, t, up, down, ring);
-    else if (warp >= kEpiWarp0)
-      epilogue<false, 0>(p, t, up, down, ring);
+    else if (warp >= (a.lora.n > 0 ? kLoraWarp0 : kEpiWarp0)) {
+      if (a.terms == 2)
+        epilogue<true, 2>(p, t, up, down, ring);
+      else if (a.terms == 1)
+        epilogue<true, 1>(p, t, up, down, ring);
+      else if (pair)
+        epilogue<true, 0>(p, t, up, down, ring);
+      else
+        epilogue<false, 0>(p, t, up, down, ring);
+    }
     __syncwarp();
   }
   tc_fence_before();
