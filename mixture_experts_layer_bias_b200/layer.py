@@ -24,6 +24,13 @@ class MoELayer:
         self.weights = ops.make_weights(weights)
         self.adapter_tensors = adapters
         self.lora = None if adapters is None else ops.make_lora(adapters)
+        if adapters is not None:
+            for f, (rows, cols) in dict(a_gate=(None, cfg.d), a_up=(None, cfg.d), a_down=(None, cfg.h), b_gate=(cfg.h, None),
+                                        b_up=(cfg.h, None), b_down=(cfg.d, None)).items():
+                t = adapters.get(f)
+                if t is not None and (t.shape[1] != cfg.E + cfg.num_shared or (rows or t.shape[2]) != t.shape[2]
+                                      or (cols or t.shape[3]) != t.shape[3]):
+                    raise ValueError(f"{f} is not of this layer's experts, width or hidden width")
         if self.lora is None:
             nbytes = ops.moe_workspace_size(self.desc)
         else:
@@ -50,16 +57,26 @@ class MoELayer:
             raise ValueError("adapter_ids must be a contiguous int32 tensor [S]")
         return adapter_ids
 
+    def _checked(self, x, out, ids):
+        for t in (x, out):
+            if t.dtype != self.y.dtype or tuple(t.shape) != tuple(self.y.shape) or not t.is_contiguous() \
+                    or t.device != self.y.device:
+                raise ValueError("x and y must be contiguous tensors [S][d] of the layer's type on its device")
+        if ids is not None and ids.device != self.y.device:
+            raise ValueError("adapter_ids must lie on the layer's device")
+
     def decode(self, x: torch.Tensor, y: torch.Tensor = None, stream=None, adapter_ids=None) -> torch.Tensor:
         """The layer for a few tokens (S <= ops.MOE_DECODE_MAX_TOKENS) in one kernel."""
         out = self.y if y is None else y
-        ops.moe_layer_decode(self.desc, self.weights, self.lora, self._ids(adapter_ids), x, out, self.topk_idx,
-                             self.topk_w, self.counts, self.ws, stream)
+        self._checked(x, out, self._ids(adapter_ids))
+        ops.moe_layer_decode(self.desc, self.weights, self.lora, adapter_ids, x, out, self.topk_idx, self.topk_w,
+                             self.counts, self.ws, stream)
         return out
 
     def forward(self, x: torch.Tensor, y: torch.Tensor = None, stream=None, adapter_ids=None) -> torch.Tensor:
         out = self.y if y is None else y
         if self._ids(adapter_ids) is not None:
+            self._checked(x, out, adapter_ids)
             ops.moe_layer_forward_lora(self.desc, self.weights, self.lora, adapter_ids, x, out, self.topk_idx,
                                        self.topk_w, self.counts, self.ws, stream)
             return out

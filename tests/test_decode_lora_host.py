@@ -175,3 +175,12 @@ def test_make_lora_checks_types_and_shapes():
             ops.make_lora(dict(ad, **bad))
     with pytest.raises(ValueError):
         ops.make_lora(dict(scale=ad["scale"]))
+
+
+def test_layer_refuses_adapters_of_another_layer():
+    from mixture_experts_layer_bias_b200.layer import MoELayer
+    cfg = syn.scaled(syn.CONFIGS["mixtral_decode"], S=2, d=64, h=32, E=4)
+    for other in (dict(d=32), dict(h=64), dict(E=8)):
+        with pytest.raises(ValueError):
+            MoELayer(cfg, {}, adapters=make_adapters(syn.scaled(cfg, S=2, **dict(dict(d=64, h=32, E=4), **other)), 3, 8,
+                                                     device="cpu"))

@@ -311,3 +311,13 @@ def test_refusals():
         adapted.decode(inp["x"])
     with pytest.raises(ValueError):
         adapted.decode(inp["x"], adapter_ids=make_ids(5, 2))
+    x = inp["x"]
+    for bad in (x[:3], x.float(), x.t().contiguous().t(), x.cpu()):
+        with pytest.raises(ValueError):
+            layer.decode(bad)
+        with pytest.raises(ValueError):
+            adapted.forward(bad, adapter_ids=make_ids(4, 2))
+    with pytest.raises(ValueError):
+        layer.decode(x, y=torch.empty((5, cfg.d), dtype=x.dtype, device="cuda"))
+    with pytest.raises(ValueError):
+        adapted.decode(x, adapter_ids=make_ids(4, 2, device="cpu"))
