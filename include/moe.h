@@ -407,8 +407,9 @@ moe_status moe_layer_forward_timed(const moe_desc *desc, const moe_weights *w, c
 /*
  * The whole layer for a few tokens in ONE kernel: S <= MOE_DECODE_MAX_TOKENS.
  * Same arguments, weights and results as moe_layer_forward (up to fp32
- * summation order; router logits and selection keys are fp64 here), plus optional adapters (lora and adapter_of_token, both
- * NULL or both given).  The expert outputs are summed in fp32 (no bf16
+ * summation order; router logits and selection keys are fp64 here), plus
+ * optional adapters (lora and adapter_of_token, both NULL or both given).  The
+ * expert outputs are summed in fp32 (no bf16
  * rounding per expert); the hidden rows are bf16 (two-term or W8A8 codes with
  * E4M3 weights), as in moe_grouped_ffn.  A capacity changes nothing (no row
  * is dropped; MOE_CNT_OVERFLOW_ROWS is not counted).
@@ -441,9 +442,10 @@ moe_status moe_layer_decode(const moe_desc *desc, const moe_weights *w, const mo
  * plus lora and adapter_of_token; where two keys are too close for fp32 sums to
  * tell, it selects on fp64 logits and keys, as moe_layer_decode does throughout
  * (moe_route: fp32), so such experts may be picked differently from the staged
- * calls.  The
- * adapters' inner products A x are summed in fp32 and kept as bf16 between the
- * two products, their share of a sum is bf16.  ws: at least
+ * calls.  The adapters' inner products A x are summed in fp32 and kept as bf16
+ * between the two products, their share of a sum is bf16.  Groups of offsets that
+ * claim more rows than S * K + num_shared * S together, more than S each, or rows
+ * behind R go without adapters and set MOE_STATUS_BAD_GROUP.  ws: at least
  * moe_lora_workspace_size bytes, otherwise as moe_layer_forward.  reroute = 1
  * is supported by both as by the calls without adapters.
  */
