@@ -2,8 +2,11 @@
 // for any number of tokens.
 //
 // The logits are tensor-core products (m16n8k16, fp32 sums): a CTA takes 16
-// tokens, its eight warps split d and add up in warp order, so a sum is only
-// d / 128 + 8 additions long.  Each warp then selects two of the tokens in fp32.
+// tokens, its eight warps split d and add up in warp order.  The instruction
+// sums 32 columns at a time, from zero, and ordinary fp32 additions join those
+// sums: what it may lose of its addends is then a share of those 32 products,
+// not of all that came before them (see logit_tol).  Each warp then selects two
+// of the tokens in fp32.
 // Where two of a token's K + 1 best keys (or the last kept and the first dropped
 // group) lie closer than a bound on those sums' errors allows to tell, it selects
 // in fp64, with the logits of the experts in question summed again in fp64 (a
@@ -261,8 +264,11 @@ __device__ void tile_logits(const ExactParams& p, int t0, int e0, float (*part)[
       for (int v = 0; v < 8; ++v) xs[i] = fmaf(bf16_at(pc.a[i], v), bf16_at(pc.a[i], v), xs[i]);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      mma_bf16(acc[j], pc.a[0].x, pc.a[1].x, pc.a[0].y, pc.a[1].y, pc.b[j].x, pc.b[j].y);
-      mma_bf16(acc[j], pc.a[0].z, pc.a[1].z, pc.a[0].w, pc.a[1].w, pc.b[j].z, pc.b[j].w);
+      float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // (from zero: logit_tol counts on it)
+      mma_bf16(c, pc.a[0].x, pc.a[1].x, pc.a[0].y, pc.a[1].y, pc.b[j].x, pc.b[j].y);
+      mma_bf16(c, pc.a[0].z, pc.a[1].z, pc.a[0].w, pc.a[1].w, pc.b[j].z, pc.b[j].w);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[j][v] += c[v];
     }
   };
   constexpr int kAhead = NT <= 2 ? 4 : 2;  // pieces in flight
@@ -297,15 +303,24 @@ __device__ void tile_logits(const ExactParams& p, int t0, int e0, float (*part)[
   __syncthreads();
 }
 
-// Bound on the errors of a token's fp32 logits: a sum has d / 128 + 8 additions
-// (16 products at a time in the tensor cores), each off by at most 2^-22 of its
-// largest part, which is at most |x| |w|.  Twice that.
+// Bound on the errors of a token's fp32 logits, in units of u = 2^-24 |x| |w|.
+//   32 columns: two instructions of 16 products and an accumulator.  PTX promises
+//   additions of at least single precision in any order and with any rounding, so
+//   each is off by at most 2^-23 of its addends' magnitudes: (15 + 16) 2^-23 m with
+//   m the sum of the 32 products' magnitudes.  (Seen on a B200: addends cut to
+//   2^-25 of the largest, the sum to 2^-23: less than that.)  Over all columns the m
+//   add up to at most |x| |w|: 62 u.
+//   Joining them: a rounding of 2^-24 of a partial sum, itself at most |x| |w|, for
+//   every 256 columns (eight warps take turns) and for the eight warps: d / 256 + 9 u.
+// With room for the second-order terms 96 + d / 256 u; the last factor covers the
+// lengths' own fp32 sums (chains of d / 32 additions).
 __device__ __forceinline__ float logit_tol(const ExactParams& p, float xsq) {
   float w = 0.0f;
   for (int e = lane_id(); e < p.E; e += 32) w = fmaxf(w, __ldg(p.wsq + e));
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) w = fmaxf(w, __shfl_xor_sync(kFull, w, off));
-  return 2.0f * static_cast<float>(p.d / 128 + 16) * 0x1p-22f * sqrtf(xsq * w);
+  const float d = static_cast<float>(p.d);
+  return (d * 0x1p-8f + 96.0f) * 0x1p-24f * (1.01f + d * 0x1p-28f) * sqrtf(xsq * w);
 }
 
 // The token's selection by one warp, from its fp32 logits (without the bias), in
