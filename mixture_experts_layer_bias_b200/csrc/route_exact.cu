@@ -312,15 +312,19 @@ __device__ void tile_logits(const ExactParams& p, int t0, int e0, float (*part)[
 //   add up to at most |x| |w|: 62 u.
 //   Joining them: a rounding of 2^-24 of a partial sum, itself at most |x| |w|, for
 //   every 256 columns (eight warps take turns) and for the eight warps: d / 256 + 9 u.
-// With room for the second-order terms 96 + d / 256 u; the last factor covers the
-// lengths' own fp32 sums (chains of d / 32 additions).
+// With room for the second-order terms 96 + d / 256 u; the factor behind covers the
+// lengths' own fp32 sums (chains of d / 32 additions).  Squares below fp32's range
+// (elements below 2^-74) take less than 2^-58 from a length for any 32-bit d, products
+// below it less than 2^-95 from a sum; squares above it make the bound infinite, which
+// decides nothing.
 __device__ __forceinline__ float logit_tol(const ExactParams& p, float xsq) {
   float w = 0.0f;
   for (int e = lane_id(); e < p.E; e += 32) w = fmaxf(w, __ldg(p.wsq + e));
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) w = fmaxf(w, __shfl_xor_sync(kFull, w, off));
   const float d = static_cast<float>(p.d);
-  return (d * 0x1p-8f + 96.0f) * 0x1p-24f * (1.01f + d * 0x1p-28f) * sqrtf(xsq * w);
+  return (d * 0x1p-8f + 96.0f) * 0x1p-24f * (1.01f + d * 0x1p-28f) * (sqrtf(xsq) + 0x1p-58f) * (sqrtf(w) + 0x1p-58f) +
+         0x1p-95f;
 }
 
 // The token's selection by one warp, from its fp32 logits (without the bias), in

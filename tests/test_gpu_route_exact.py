@@ -91,7 +91,7 @@ def test_sums_that_lose_every_product_in_opposite_directions():
     products below a sum's last bit to it, expert 1 subtracts some, and three
     further columns give expert 1 all of that back but for a tiny rest: at
     65,536 columns a sum that drops the small products is off by more than
-    2^-9 of its size."""
+    2^-12 of its size."""
     d, unit = 65536, 2.0 ** -24
     x, w = np.zeros((64, d)), np.zeros((8, d))
     x[:, 256:] = 2.0 ** -12
@@ -129,3 +129,15 @@ def _cancelling(scale, d=4096):
 def test_large_products_that_cancel():
     x, w = _cancelling(1.0)
     _check(dataclasses.replace(BASE, d=4096), x, w, close=0.5)
+
+
+@pytest.mark.parametrize("exponent", [-40, -90, 40, 60])
+def test_large_products_that_cancel_at_any_scale(exponent):
+    x, w = _cancelling(2.0 ** exponent)
+    _check(dataclasses.replace(BASE, d=4096), x, w, close=0.5)
+
+
+def test_cancelling_products_of_small_rows_and_small_router_weights():
+    """x and w at scales whose lengths' product still is a normal number but whose squares' product is not."""
+    x, w = _cancelling(2.0 ** -45)
+    _check(dataclasses.replace(BASE, d=4096), x, (w.float() * 2.0 ** -40).bfloat16(), close=0.5)
