@@ -354,10 +354,11 @@ __device__ bool select_fast(const ExactParams& p, int tok, const float* approx, 
     if (!valid[i]) key[i] = kNegInf;
     bad |= valid[i] && !isfinite(key[i]);
     cand[i] = valid[i];
-    if (valid[i]) top = fmaxf(top, fabsf(key[i]) + fabsf(l));
+    if (valid[i]) top = fmaxf(top, fabsf(key[i]) + fabsf(score[i]) + fabsf(l));
   }
   if (__any_sync(kFull, bad)) return false;
-  // a key's error: the logit's, and the roundings of the bias, the score and the selection bias
+  // a key's error: the logit's, and the roundings of the router bias, the score (which repeats the one before it 1 / tau
+  // times as large) and the selection bias, each of a few 2^-24 of its own result: a large score may hide in a small key
   const float err = tol * (p.score_fn == MOE_SCORE_SIGMOID ? 0.25f : 1.0f / p.tau) + warp_max(top) * 0x1p-21f;
   if (p.num_groups > 1) {
     const int gs = p.E / p.num_groups;

@@ -141,3 +141,28 @@ def test_cancelling_products_of_small_rows_and_small_router_weights():
     """x and w at scales whose lengths' product still is a normal number but whose squares' product is not."""
     x, w = _cancelling(2.0 ** -45)
     _check(dataclasses.replace(BASE, d=4096), x, (w.float() * 2.0 ** -40).bfloat16(), close=0.5)
+
+
+def test_a_selection_bias_that_cancels_a_large_tempered_score():
+    """score = (x w + router bias) / tau around 10^5, the selection bias takes
+    all but 1024 x w of it away: the score's fp32 steps are larger than the gaps."""
+    rng = np.random.default_rng(8)
+    d = 256
+    x, w = np.zeros((64, d)), np.zeros((8, d))
+    x[:, :8] = rng.normal(size=(64, 8))
+    w[:, :8] = rng.normal(size=(8, 8)) * 8e-6
+    rb = torch.tensor(2.0 ** (4 + 4 * rng.random(8)), dtype=torch.float32)  # of several sizes: steps of several sizes
+    sb = rb * -1024.0  # exact
+    _check(dataclasses.replace(BASE, d=d, temperature=2.0 ** -10), _bf16(x), _bf16(w), rb, sb, close=0.5)
+
+
+def test_a_selection_bias_that_cancels_sigmoid_scores():
+    """Scores around 1/2 whose differences of about 1e-7 the selection bias lays bare."""
+    rng = np.random.default_rng(9)
+    d = 256
+    x, w = np.zeros((64, d)), np.zeros((8, d))
+    x[:, :8] = rng.normal(size=(64, 8))
+    w[:, :8] = rng.normal(size=(8, 8)) * 4e-7
+    rb = torch.tensor(0.02 * rng.random(8) - 0.01, dtype=torch.float32)
+    sb = torch.tensor(-1 / (1 + np.exp(-np64(rb))), dtype=torch.float32)
+    _check(dataclasses.replace(BASE, d=d, score_fn=syn.SIGMOID), _bf16(x), _bf16(w), rb, sb, close=0.5)
