@@ -31,6 +31,11 @@ class MoELayer:
                 if t is not None and (t.shape[1] != cfg.E + cfg.num_shared or (rows or t.shape[2]) != t.shape[2]
                                       or (cols or t.shape[3]) != t.shape[3]):
                     raise ValueError(f"{f} is not of this layer's experts, width or hidden width")
+            # the library takes their addresses as they are: memory of another device would fault
+            for f in ops.LORA_FIELDS:
+                t = adapters.get(f)
+                if t is not None and not self._holds(t):
+                    raise ValueError(f"{f} lies on {t.device}, not on the layer's device")
         if self.lora is None:
             nbytes = ops.moe_workspace_size(self.desc)
         else:
@@ -48,6 +53,11 @@ class MoELayer:
             self.topk_idx = torch.empty((self.S, cfg.K), dtype=torch.int32, device=self.device)
             self.topk_w = torch.empty((self.S, cfg.K), dtype=torch.float32, device=self.device)
             self.counts = torch.empty((cfg.E,), dtype=torch.int32, device=self.device)
+
+    def _holds(self, t):
+        if t.device.type != "cuda" or self.device.type != "cuda":
+            return t.device == self.device
+        return t.device.index == (torch.cuda.current_device() if self.device.index is None else self.device.index)
 
     def _ids(self, adapter_ids):
         if (adapter_ids is None) != (self.lora is None):

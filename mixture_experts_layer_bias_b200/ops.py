@@ -141,8 +141,8 @@ def make_weights(tensors: dict) -> MoeWeights:
 def make_lora(tensors: dict) -> MoeLora:
     """Adapters struct from a dict of bf16 tensors a_gate [N][E+ns][r][d],
     b_gate [N][E+ns][h][r], a_up, b_up, a_down, b_down (missing pairs -> NULL)
-    and scale fp32 [N]; the number of adapters and the rank come from their
-    shapes.  The caller keeps the tensors alive."""
+    and scale fp32 [N], all on one device; the number of adapters and the rank
+    come from their shapes.  The caller keeps the tensors alive."""
     first = next((tensors[f] for f in LORA_FIELDS if f.startswith("a_") and tensors.get(f) is not None), None)
     if first is None:
         raise ValueError("make_lora: no adapter pair given")
@@ -154,11 +154,15 @@ def make_lora(tensors: dict) -> MoeLora:
     for f in LORA_FIELDS:
         t = tensors.get(f)
         if t is not None:
+            if t.dim() != (1 if f == "scale" else 4):
+                raise ValueError(f"make_lora: {f} has the wrong number of dimensions")
             want = torch.float32 if f == "scale" else torch.bfloat16
             shape = (lora.num_adapters,) if f == "scale" else (lora.num_adapters, slabs, t.shape[2], t.shape[3])
             rank = lora.rank if f == "scale" else t.shape[2 if f.startswith("a_") else 3]
             if t.dtype != want or tuple(t.shape) != shape or rank != lora.rank or not t.is_contiguous():
                 raise ValueError(f"make_lora: {f} has the wrong type, shape or layout")
+            if t.device != first.device:
+                raise ValueError(f"make_lora: {f} lies on {t.device}, not on {first.device}")
         setattr(lora, f, _ptr(t))
     return lora
 

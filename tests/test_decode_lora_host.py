@@ -184,3 +184,21 @@ def test_layer_refuses_adapters_of_another_layer():
         with pytest.raises(ValueError):
             MoELayer(cfg, {}, adapters=make_adapters(syn.scaled(cfg, S=2, **dict(dict(d=64, h=32, E=4), **other)), 3, 8,
                                                      device="cpu"))
+
+
+def test_adapters_on_another_device_are_refused():
+    """Their addresses go to the kernels as they are, so this is refused before anything is made or launched."""
+    from mixture_experts_layer_bias_b200.layer import MoELayer
+    cfg = syn.scaled(syn.CONFIGS["mixtral_decode"], S=2, d=64, h=32, E=4)
+    ad = make_adapters(cfg, 3, 8, device="cpu")
+    with pytest.raises(ValueError, match="device"):
+        MoELayer(cfg, {}, adapters=ad)  # on the GPU by default
+    for f in ("scale", "b_up", "a_down"):
+        with pytest.raises(ValueError, match=f"{f} lies on"):
+            ops.make_lora(dict(ad, **{f: ad[f].to("meta")}))
+    with pytest.raises(ValueError):
+        ops.make_lora(dict(ad, a_gate=ad["a_gate"][0]))
+    with pytest.raises(ValueError):
+        ops.make_lora(dict(ad, b_down=ad["b_down"][0]))
+    with pytest.raises(ValueError):
+        ops.make_lora(dict(ad, scale=ad["scale"][:, None]))
