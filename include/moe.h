@@ -416,7 +416,7 @@ moe_status moe_layer_forward_timed(const moe_desc *desc, const moe_weights *w, c
  *   Supported: bf16 activations with bf16 weights (SwiGLU, GeLU) or E4M3
  *   weights (SwiGLU, act_quant 0 or 1, d and h multiples of 16), reroute = 0;
  *   MOE_ERR_UNSUPPORTED otherwise, and for layers too large for the kernel's
- *   tables (min(E, S * K) + num_shared experts of up to 20 M / that many
+ *   tables (min(E, S * K) + num_shared experts of up to 18 M / that many
  *   columns of d always fit, and 2^30 tiles of 128 x 64 weights);
  *   MOE_ERR_INVALID_ARG for a larger S.
  *   ws: at least moe_decode_workspace_size bytes (lora may be NULL there),

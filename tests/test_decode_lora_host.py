@@ -202,3 +202,24 @@ def test_adapters_on_another_device_are_refused():
         ops.make_lora(dict(ad, b_down=ad["b_down"][0]))
     with pytest.raises(ValueError):
         ops.make_lora(dict(ad, scale=ad["scale"][:, None]))
+
+
+def test_decode_takes_every_width_that_its_header_promises():
+    """moe.h: min(E, S * K) + num_shared experts of up to so many million / that many columns of d always fit."""
+    import os
+    import re
+    text = open(os.path.join(B.INCLUDE, "moe.h")).read()
+    promised = int(re.search(r"up to (\d+) M / that many", re.sub(r"[\s*]+", " ", text)).group(1)) * 1_000_000
+    refused = []
+    for over in (dict(), dict(weight_dtype=syn.E4M3), dict(weight_dtype=syn.E4M3, act_quant=1)):
+        for E in (8, 32, 256):
+            for ns in (0, 1):
+                for S in range(1, 65):
+                    for K in (1, 2, 8, 24, 29, 30, 31, 32):
+                        if K > E:
+                            continue
+                        d = promised // (min(E, S * K) + ns) // 16 * 16
+                        desc = _desc(num_tokens=S, num_experts=E, top_k=K, num_shared=ns, d_model=d, d_ff=16, **over)
+                        if _size_code(desc) != ops.MOE_OK:
+                            refused.append((over, E, ns, S, K, d))
+    assert not refused, (len(refused), refused[:4])
