@@ -438,7 +438,7 @@ moe_status moe_layer_decode(const moe_desc *desc, const moe_weights *w, const mo
  * The grouped expert FFN and the whole layer with adapters, for any number of
  * tokens.  moe_grouped_ffn_lora: moe_grouped_ffn's arguments plus lora,
  * adapter_of_token [S] and token_of_row [R] (moe_permute's output; rows with
- * -1 are not computed).  moe_layer_forward_lora: moe_layer_forward's arguments
+ * -1 get no adapter's share).  moe_layer_forward_lora: moe_layer_forward's arguments
  * plus lora and adapter_of_token; where two keys are too close for fp32 sums to
  * tell, it selects on fp64 logits and keys, as moe_layer_decode does throughout
  * (moe_route: fp32), so such experts may be picked differently from the staged
@@ -447,7 +447,9 @@ moe_status moe_layer_decode(const moe_desc *desc, const moe_weights *w, const mo
  * claim more rows than S * K + num_shared * S together, more than S each, or rows
  * behind R go without adapters and set MOE_STATUS_BAD_GROUP.  ws: at least
  * moe_lora_workspace_size bytes, otherwise as moe_layer_forward.  reroute = 1
- * is supported by both as by the calls without adapters.
+ * is supported by both as by the calls without adapters: the first choices are
+ * those of the exact keys, the slots that move go by the keys in fp32 and take
+ * their gates from scores in fp32.
  */
 moe_status moe_lora_workspace_size(const moe_desc *desc, const moe_lora *lora, size_t *bytes);
 moe_status moe_grouped_ffn_lora(const moe_desc *desc, const moe_weights *w, const moe_lora *lora,
