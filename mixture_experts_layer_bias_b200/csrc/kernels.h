@@ -45,8 +45,6 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
 // The same selection for bf16 layers, decided by fp64 keys where fp32 ones are
 // too close to tell.  wsq: scratch [E]; zero: four words set to zero on the way.
 cudaError_t launch_route_exact(const RouteArgs& a, float* wsq, int* zero, cudaStream_t stream);
-// x W_r^T alone, into logits_scratch.
-cudaError_t launch_router_logits(const RouteArgs& a, cudaStream_t stream);
 
 // --- over-capacity re-routing ------------------------------------------------
 // Excess slots (row_of_slot >= E*C after a capacity-bounded permutation) move,

@@ -442,8 +442,6 @@ cudaError_t launch_route_rows_f32(const RouteArgs& a, const SelectParams& sp, cu
   return cudaGetLastError();
 }
 
-}  // namespace
-
 // x W_r^T into logits_scratch (the router bias is added by the selection).
 cudaError_t launch_router_logits(const RouteArgs& a, cudaStream_t stream) {
   // bf16: one dense GEMM on the tensor cores (fp32 accumulate and output, which
@@ -479,6 +477,8 @@ cudaError_t launch_router_logits(const RouteArgs& a, cudaStream_t stream) {
                                                     static_cast<const float*>(a.w_router), a.logits_scratch);
   return cudaGetLastError();
 }
+
+}  // namespace
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
   if (a.S == 0) return cudaSuccess;

@@ -117,17 +117,13 @@ __device__ void exact_logits(const ExactParams& p, const __nv_bfloat16* xr, cons
 template <int NI>
 struct Token {
   double logit[NI];  // expert 32 i + lane
-  uint32_t exact;    // bit i: logit[i] is exact
 };
 
 template <int NI>
 __device__ __forceinline__ void put(Token<NI>& t, int e, double v) {
 #pragma unroll
   for (int i = 0; i < NI; ++i)
-    if (32 * i + lane_id() == e) {
-      t.logit[i] = v;
-      t.exact |= 1u << i;
-    }
+    if (32 * i + lane_id() == e) t.logit[i] = v;
 }
 
 __device__ __forceinline__ double score_of(const ExactParams& p, double l) {
@@ -454,7 +450,6 @@ __device__ __noinline__ void select_token(const ExactParams& p, int tok, const f
   const int lane = lane_id();
   const __nv_bfloat16* xr = p.x + static_cast<int64_t>(tok) * p.d;
   Token<NI> t;
-  t.exact = 0;
   double key[NI];
   bool cand[NI], valid[NI];
   double gap;
