@@ -307,7 +307,9 @@ LoraLayout lora_layout(const moe_desc& d, const moe_lora& l) {
   L.tiles = take(used * sizeof(LoraTile));
   L.list = take(kLoraTileRows * used * sizeof(int2));
   L.has = take(rows);
-  L.u = take(kLoraMaxSplits * used * pairs * l.rank * 4);
+  // inner products, by slice of their length: of gate and up (width d), then of down (h)
+  const int64_t u_up = lora_splits(used, d.d_model, kLoraMaxSms) * pairs, u_down = lora_splits(used, d.d_ff, kLoraMaxSms);
+  L.u = take((u_up > u_down ? u_up : u_down) * used * l.rank * 4);
   L.delta = take(rows * cols * 2);
   L.wsq = take(d.num_experts * 4);
   L.total = o;

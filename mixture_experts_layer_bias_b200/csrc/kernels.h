@@ -198,6 +198,18 @@ struct LoraParams {
 constexpr int kLoraTileRows = 32;
 constexpr int kLoraMaxAdapters = MOE_LORA_MAX_ADAPTERS;
 constexpr int kLoraMaxSplits = 8;
+constexpr int kLoraMaxSms = 160;  // the workspace has room for what this many SMs want
+
+// Slices of the length K in the inner products of `rows` rows: about four units
+// per SM when every tile is full, at least 256 k each.
+inline int lora_splits(int64_t rows, int K, int num_sms) {
+  const int64_t tiles = (rows + kLoraTileRows - 1) / kLoraTileRows;
+  if (tiles <= 0) return 1;
+  int64_t splits = (4 * (num_sms < kLoraMaxSms ? num_sms : kLoraMaxSms) + tiles - 1) / tiles;
+  if (splits > kLoraMaxSplits) splits = kLoraMaxSplits;
+  if (splits > K / 256) splits = K / 256 > 0 ? K / 256 : 1;
+  return static_cast<int>(splits);
+}
 struct LoraTile {
   int expert, adapter, pos, rows;  // its inner products: rows pos .. pos + rows - 1 of u
 };

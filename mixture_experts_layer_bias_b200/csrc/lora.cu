@@ -459,11 +459,7 @@ cudaError_t launch_lora_plan(const LoraPlanArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_lora_rows(const LoraRowsArgs& a, cudaStream_t stream) {
   if (a.max_total_rows <= 0) return cudaSuccess;
-  // slices of K: about four units per SM when every tile is full, at least 256 k each
-  const int64_t tiles = (a.max_total_rows + kRows - 1) / kRows;
-  int splits = static_cast<int>((4 * a.num_sms + tiles - 1) / tiles);
-  if (splits > kLoraMaxSplits) splits = kLoraMaxSplits;
-  if (splits > a.K / 256) splits = a.K / 256 > 0 ? a.K / 256 : 1;
+  int splits = lora_splits(a.max_total_rows, a.K, a.num_sms);
   const int chunk = ((a.K + splits - 1) / splits + 31) & ~31;
   splits = (a.K + chunk - 1) / chunk;
   const int nb = (a.pairs * a.lora.r + 31) / 32;

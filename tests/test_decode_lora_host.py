@@ -223,3 +223,15 @@ def test_decode_takes_every_width_that_its_header_promises():
                         if _size_code(desc) != ops.MOE_OK:
                             refused.append((over, E, ns, S, K, d))
     assert not refused, (len(refused), refused[:4])
+
+
+def test_adapters_workspace_holds_the_slices_that_are_used():
+    """The inner products lie there by slice of their length: eight of them in small batches, one in large ones."""
+    def bytes_per_rank(**over):
+        d = _desc("mixtral_prefill", **over)
+        return (ops.moe_lora_workspace_size(d, _lora(rank=128)) - ops.moe_lora_workspace_size(d, _lora(rank=64))) / 64
+    rows = 16384 * 8
+    assert bytes_per_rank(num_tokens=16384, num_experts=64, top_k=8) == rows * 2 * 4
+    assert bytes_per_rank(num_tokens=64, top_k=2) == 8 * 64 * 2 * 2 * 4
+    # a hidden width of 512 has two slices of 256, its one pair half as many products a slice as gate and up have
+    assert bytes_per_rank(num_tokens=64, top_k=2, d_model=256, d_ff=512) == 64 * 2 * 2 * 4
