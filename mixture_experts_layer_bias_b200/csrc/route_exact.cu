@@ -10,14 +10,22 @@
 // Where two of a token's K + 1 best keys (or the last kept and the first dropped
 // group) lie closer than a bound on those sums' errors allows to tell, it selects
 // in fp64, with the logits of the experts in question summed again in fp64 (a
-// product of two bf16 numbers is exact in fp32); that is a few tokens in a
-// hundred.
-//
-// 38 us for 3001 tokens of width 2048 and 64 experts, 23 us for 2048 tokens of width
-// 4096 and 8 experts, inside the layer (reading x: 2 to 3 us): what is left is the
-// few fp64 tokens, each a chain of about 8 us, one of which most CTAs have.  The
-// squared lengths of the router's rows, made in this kernel on the way, took 66 us
-// where the kernel of their own and this one take 46.
+// product of two bf16 numbers is exact in fp32).  How often that is, for random
+// rows, and what the kernel takes with 2048 of them (the second line: 3001):
+//     8 experts, width 4096                       0.6 % of the tokens     24 us
+//    64 experts, width 2048                       4 %                     46 us
+//   128 experts, width 4096, 2 of 4 groups        10 %                   279 us
+//   256 experts, width 7168                       14 %                   295 us
+//   256 experts, width 7168, 2 of 8 groups        14 %                  1152 us
+// Reading x takes 2 to 5 us; in the narrow routers what is left is the few fp64
+// tokens, each a chain of about 8 us, one of which most CTAs have.  With groups one
+// token in 100 (4 groups) or 50 (8 groups) leaves open which groups are kept: its
+// warp then sums every expert's logit, two at a time, and the launch lasts as long as
+// that takes.  Without fresh sums every 32 columns the bound has to be three to five
+// times larger and grows with the width (and with the smaller bound that the kernel
+// once had, which did not hold, the last line took 1794 us, the fourth 215).  The
+// squared lengths of the router's rows, made in this kernel on the way, cost 20 us
+// more than in a kernel of their own (64 experts).
 //
 // Scores, selection bias, group limit and gates as in the routing kernels
 // (jsqmd.com "第11章 MoE模型推理" 11.1.1, 11.3.3; ybb.press "MoE 推理工程深层实战"
@@ -258,14 +266,19 @@ __device__ void tile_logits(const ExactParams& p, int t0, int e0, float (*part)[
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int v = 0; v < 8; ++v) xs[i] = fmaf(bf16_at(pc.a[i], v), bf16_at(pc.a[i], v), xs[i]);
+    float c[NT][4];  // from zero: logit_tol counts on it; all first halves, then all second ones, so that none waits
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // (from zero: logit_tol counts on it)
-      mma_bf16(c, pc.a[0].x, pc.a[1].x, pc.a[0].y, pc.a[1].y, pc.b[j].x, pc.b[j].y);
-      mma_bf16(c, pc.a[0].z, pc.a[1].z, pc.a[0].w, pc.a[1].w, pc.b[j].z, pc.b[j].w);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) acc[j][v] += c[v];
+      for (int v = 0; v < 4; ++v) c[j][v] = 0.0f;
+      mma_bf16(c[j], pc.a[0].x, pc.a[1].x, pc.a[0].y, pc.a[1].y, pc.b[j].x, pc.b[j].y);
     }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) mma_bf16(c[j], pc.a[0].z, pc.a[1].z, pc.a[0].w, pc.a[1].w, pc.b[j].z, pc.b[j].w);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[j][v] += c[j][v];
   };
   constexpr int kAhead = NT <= 2 ? 4 : 2;  // pieces in flight
   Piece pc[kAhead];
