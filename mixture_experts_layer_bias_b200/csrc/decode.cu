@@ -500,7 +500,8 @@ __device__ void select_tokens(const Params& p, Scratch& c, int t0, int n, int wi
 // What a step of a group with this many tokens costs: its weight bytes and, for
 // every 16 columns of its token tile, about a tenth of that again (measured on 64
 // tokens over 64 E4M3 experts: 52 us for a CTA's steps with one box of columns, 67
-// with three, 75 with five).  Groups that share a dense tile all cost the same.
+// with three, 75 with five; that shape alone is behind the numbers, bf16 weights and
+// other widths use them as they are).  Groups that share a dense tile all cost the same.
 __device__ __forceinline__ int step_cost(const DecodeArgs& a, int tokens) {
   return all_tokens(a.S, a.terms) ? 1 : 9 + (tokens * (a.terms == 2 ? 2 : 1) + 15) / 16;
 }

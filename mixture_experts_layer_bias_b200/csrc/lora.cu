@@ -164,11 +164,13 @@ __device__ __forceinline__ void meta_store(TileRows& t, const MetaRegs& m) {
 // pieces of 32 k with the next piece's loads under way during a piece's products;
 // the warps of a block add up in a fixed order through shared memory.  (With 16
 // warps per SM the loop is bound by its own instructions as much as by loads, so
-// the whole pieces have no conditions and constant offsets.)  Measured inside the
-// layer on 27,009 rows over 65 E4M3 experts, 12 adapters of rank 32: 71 us for gate
-// and up (K = 2048; 204 MB of matrices from HBM, 31 us), 75 us for down (K = 1408).
-// What bounds it is the way from L2: a tile of 32 rows reads its 64 (or 32) rows of
-// A again, and a load of a fragment touches eight lines.
+// the whole pieces have no conditions and constant offsets.  Two pieces of fragments
+// beside the accumulators and pointers are more than the 128 registers that 16 warps
+// leave a thread: it spills 432 bytes, 244 with eight warps to a CTA.)  Measured
+// inside the layer on 24,008 rows over 64 E4M3 experts, 12 adapters of rank 32: 62 us
+// for gate and up (K = 2048; 215 MB from HBM, 33 us at the copy rate), 38 us for down
+// (K = 1408; 132 MB, 20 us).  What bounds it is the way from L2: a tile of 32 rows
+// reads its 64 (or 32) rows of A again, and a load of a fragment touches eight lines.
 template <int V>
 struct Const {
   static constexpr int value = V;
@@ -324,10 +326,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lora_inner_kernel(const LoraRo
 // makes 32 columns of a pair at a time, the next columns' rows of B under way
 // during the products.  Its column c of the 8-column tile j stands for column 8
 // (c / 2) + 2 j + c % 2 of the 32, so that a lane ends with 8 neighbouring
-// columns of its rows: one 16-byte store each.  Measured as above: 88 us for gate
-// and up (N = 1408 each: 152 MB of deltas and 140 MB of matrices, 45 us), 58 us for
-// down (N = 2048).  The deltas are bf16: their rounding is a 2^-9 share of what the
-// adapters add, and fp32 ones would cost twice the traffic.
+// columns of its rows: one 16-byte store each.  Measured as above: 82 us for gate
+// and up (N = 1408 each: 125 MB of deltas and 138 MB from HBM, 40 us at the copy
+// rate), 55 us for down (N = 2048).  u is summed in fp32 over all of K and rounded
+// once, to the type that the instruction multiplies, and the deltas are bf16: each
+// rounding is at most a 2^-8 share of what the adapters add.  Two bf16 terms of u
+// would double the products, fp32 deltas the traffic that bounds this kernel.
 constexpr int kOuterThreads = 128;
 constexpr int kOuterWarps = kOuterThreads / 32;
 

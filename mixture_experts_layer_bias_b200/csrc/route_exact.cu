@@ -21,9 +21,9 @@
 // tokens, each a chain of about 8 us, one of which most CTAs have.  With groups one
 // token in 100 (4 groups) or 50 (8 groups) leaves open which groups are kept: its
 // warp then sums every expert's logit, two at a time, and the launch lasts as long as
-// that takes.  Without fresh sums every 32 columns the bound has to be three to five
-// times larger and grows with the width (and with the smaller bound that the kernel
-// once had, which did not hold, the last line took 1794 us, the fourth 215).  The
+// that takes.  (Sums carried through the whole width need a bound that is larger and
+// grows with it; under one that did not hold they took 1794 us for the last line and
+// 215 for the one before, where most of the time is now the products'.)  The
 // squared lengths of the router's rows, made in this kernel on the way, cost 20 us
 // more than in a kernel of their own (64 experts).
 //
